@@ -1,0 +1,116 @@
+/*
+ * wq_block.h -- C ABI of the block-scaled FP8 operators (MI355X, gfx950).
+ *
+ * A block-scaled tensor holds E4M3 codes (OCP, max 448) and one fp32 scale for
+ * each 128 codes along K: value = code * scale.
+ *   activations X[M][K]: codes uint8 [M][K],    scales float [M][KB], KB = ceil(K / 128);
+ *                        block kb of row m is K range [128 kb, min(128 kb + 128, K))
+ *   weights  W[E][N][K]: codes uint8 [E][N][K], scales float [E][NB][KB], NB = ceil(N / 128);
+ *                        block (nb, kb) is 128 rows x 128 K, smaller at the edges
+ *                        (a plain Linear is E = 1)
+ * The quantizer, for every block of fp32 values y:
+ *   s    = max(amax / 448, 2^-126), amax = max |y|, one IEEE fp32 division
+ *   code = E4M3(clamp(y / s, +-448)), nearest even, the sign of zero kept; the
+ *          quotient is evaluated as y * (1 / s) in fp32 (1 / s correctly rounded),
+ *          at most 1.5 fp32 ulp from y / s.  The floor 2^-126 keeps 1 / s finite:
+ *          an all-zero block has that scale and codes 0.
+ * A block that holds a NaN has the scale NaN, one that holds an infinity (and no
+ * NaN) the scale infinity: no finite value is made up for it.
+ *
+ * Conventions are those of wq.h: device pointers owned by the caller, row-major
+ * tensors, bf16 as uint16 bit patterns, stream-ordered calls that neither wait
+ * nor allocate, every check on the host before anything is enqueued,
+ * wq_last_error() for the reason.  Base pointers of codes, bf16 tensors and
+ * workspaces must be 16-byte aligned, the other pointers aligned to their type.
+ * K % 16 == 0 everywhere (WQ_ESHAPE otherwise).
+ */
+#ifndef WQ_BLOCK_H
+#define WQ_BLOCK_H
+
+#include "wq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* K elements (and weight rows) per scale. */
+#define WQ_BLOCK 128
+
+/*
+ * Quantize bf16 weights W[E][N][K] (contiguous) to codes and scales, one scale
+ * for each 128 x 128 block of each of the E matrices.  Any N.
+ */
+wq_status wq_block_quantize_weight(const void* W, int64_t E, int64_t N, int64_t K, void* codes, float* scales,
+                                   void* stream);
+
+/*
+ * Quantize bf16 rows X[M][K] (row m at X + m * ldx elements; ldx >= K,
+ * ldx % 8 == 0) to codes Xq[M][K] and scales Xs[M][KB].
+ */
+wq_status wq_block_quantize_act(const void* X, int64_t ldx, int64_t M, int64_t K, void* Xq, float* Xs, void* stream);
+
+/*
+ * Root-mean-square norm of a residual stream with a quantized result, all in
+ * fp32 from bf16 inputs:
+ *   h = x + residual (h = x without a residual)
+ *   y = h * rsqrt(mean_k h^2 + eps) * gain[k]
+ * Xq/Xs receive y quantized; residual_out (or NULL) receives bf16(h) and y_out
+ * (or NULL) bf16(y), both [M][K].  y comes from the unrounded h: rounding h to
+ * bf16 is the stored residual's alone.
+ *   X            : bf16 rows at X + m * ldx elements (ldx >= K, ldx % 8 == 0)
+ *   residual     : bf16 [M][K] or NULL
+ *   gain         : bf16 [K]
+ *   residual_out : may be the buffer of `residual` or of X (with ldx == K);
+ *                  no other overlap of outputs with inputs
+ * K <= 32768 (WQ_EUNSUPPORTED above); eps finite and >= 0.
+ */
+wq_status wq_block_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* residual, const void* gain, float eps,
+                                        int64_t M, int64_t K, void* Xq, float* Xs, void* residual_out, void* y_out,
+                                        void* stream);
+
+/*
+ * Gated activation with a quantized result: GU holds rows of 2 K bf16 values
+ * (row m at GU + m * ldg elements; ldg >= 2 K, ldg % 8 == 0), gate first;
+ *   y[k] = silu(GU[m][k]) * GU[m][K + k],  silu(g) = g / (1 + exp(-g))
+ * in fp32.  Xq/Xs receive y quantized.
+ */
+wq_status wq_block_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int64_t K, void* Xq, float* Xs,
+                                     void* stream);
+
+/*
+ * Block-scaled Linear:
+ *   Y[m][n] = bf16( sum_kb Xs[m][kb] Ws[n / 128][kb] sum_{k in kb} Xq[m][k] Wq[n][k] (+ bias[n]) )
+ * Each block's products are summed by the FP8 matrix cores in fp32, scaled and
+ * added to an fp32 sum; one rounding to bf16.  bias: bf16 [N] or NULL.  Any M
+ * and N.  Workspace: wq_block_linear_workspace bytes (0 for most shapes), no
+ * initialisation; calls that may overlap need different ones.
+ */
+size_t wq_block_linear_workspace(int64_t M, int64_t N, int64_t K);
+wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const void* Wq, const float* Ws,
+                          const void* bias, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * The same product for E experts over rows sorted by expert:
+ *   Y[t] = X[rows[t]] . W[e]^T   for offsets[e] <= t < offsets[e + 1]
+ *   Xq, Xs  : M rows of codes and scales
+ *   rows    : int32 [T] on the device, each in [0, M) (a row of another value
+ *             is read as zeros), or NULL: sorted row t reads X[t], and M == T
+ *   offsets : int32 [E + 1] on the device, nondecreasing from offsets[0] = 0;
+ *             an expert may have no rows.  Rows of Y from offsets[E] on are not
+ *             written, so T may be a buffer's capacity.
+ *   Wq, Ws  : weights of the E experts
+ *   Y       : bf16 [T][N]
+ * Nothing is read back to the host: T and E alone decide the launch.  Entries
+ * of offsets are clamped to [0, T], so no value of them reaches outside Y.
+ * M * K < 2^32 with rows (WQ_EUNSUPPORTED otherwise).
+ */
+wq_status wq_block_grouped_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const int32_t* rows,
+                                  const int32_t* offsets, int64_t T, int64_t E, const void* Wq, const float* Ws,
+                                  int64_t N, void* Y, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* WQ_BLOCK_H */

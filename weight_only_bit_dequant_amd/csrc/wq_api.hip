@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "wq.h"
+#include "wq_block_internal.hpp"
 #include "wq_internal.hpp"
 
 namespace {
@@ -559,3 +560,9 @@ wq_status wq_read_stream(const void* p, size_t bytes, uint32_t* sink, void* stre
 }
 
 }  // extern "C"
+
+// The same message store for the entry points of other files.
+namespace wq {
+wq_status api_error(wq_status st, const char* message) { return fail(st, "%s", message); }
+wq_status api_ok() { return ok(); }
+}  // namespace wq

@@ -1,0 +1,56 @@
+// Internal launch interface of the block-scaled FP8 operators
+// (wq_block_api.hip to wq_block_quant.hip and wq_block_gemm.hip).  Launchers
+// assume their arguments were validated by the ABI layer.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "wq.h"
+
+namespace wq {
+
+constexpr int kBlk = 128;  // K elements (and weight rows) per scale
+
+// Status of a call and the text of wq_last_error() (defined in wq_api.hip,
+// which holds the thread's message).
+wq_status api_error(wq_status st, const char* message);
+wq_status api_ok();
+
+constexpr int64_t kNormMaxK = 32768;  // 16 waves x 64 lanes x 4 chunks of 8
+
+struct BlockNormArgs {
+  const uint16_t* X;         // bf16 rows, ldx elements apart
+  const uint16_t* residual;  // bf16 [M][K] or null
+  const uint16_t* gain;      // bf16 [K]
+  uint8_t* Xq;               // codes [M][K]
+  float* Xs;                 // scales [M][KB]
+  uint16_t* residual_out;    // bf16 [M][K] or null
+  uint16_t* y_out;           // bf16 [M][K] or null
+  int64_t ldx;
+  int M, K;
+  float eps;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s);
+
+// gate = false: Xq/Xs = quantized rows of X[M][K]; true: of silu(X[:, :K]) * X[:, K:]
+hipError_t launch_block_quant_rows(bool gate, const uint16_t* X, int64_t ldx, int64_t M, int64_t K, uint8_t* Xq,
+                                   float* Xs, hipStream_t s);
+hipError_t launch_block_quant_weight(const uint16_t* W, int64_t E, int64_t N, int64_t K, uint8_t* codes,
+                                     float* scales, hipStream_t s);
+
+struct BlockGemmArgs {
+  const uint8_t* Xq;       // codes [M][K]
+  const float* Xs;         // scales [M][KB]
+  const uint8_t* Wq;       // codes [E][N][K]
+  const float* Ws;         // scales [E][NB][KB]
+  const uint16_t* bias;    // bf16 [N] or null
+  const int32_t* rows;     // grouped: source row of each sorted row, or null
+  const int32_t* offsets;  // grouped: [E + 1], null for a plain Linear
+  uint16_t* Y;             // bf16 [M or T][N]
+  int M, N, K, T, E;       // T: rows of Y (M for a plain Linear)
+};
+hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s);
+
+}  // namespace wq

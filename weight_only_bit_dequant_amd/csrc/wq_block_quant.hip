@@ -1,0 +1,243 @@
+// Block-scaled FP8 quantizers and the operators that end in one: activation
+// rows, residual addition + RMS norm, gated activation, weights.
+//
+// All of them read bf16 and write E4M3 codes with one fp32 scale for 128
+// elements along K, so a 16-lane row of a wave is one scale block: each lane
+// holds 8 consecutive elements (one 16-byte load, one 8-byte store of codes)
+// and the block's maximum goes round the 16 lanes by DPP row rotations,
+// without LDS.
+#include "wq_block_internal.hpp"
+#include "wq_kernel_common.hpp"
+
+namespace wq {
+
+namespace {
+
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126, the floor of a scale
+
+struct F8 {
+  float v[8];
+};
+
+__device__ __forceinline__ F8 unpack8(u32x4 w) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.v[2 * i] = bitsf(w[i] << 16);
+    f.v[2 * i + 1] = bitsf(w[i] & 0xFFFF0000u);
+  }
+  return f;
+}
+
+__device__ __forceinline__ u32x4 pack8(const F8& f) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)f32_to_bf16(f.v[2 * i]) | ((uint32_t)f32_to_bf16(f.v[2 * i + 1]) << 16);
+  return w;
+}
+
+// max of v over the 16 lanes of a DPP row (rotations by 8, 4, 2, 1)
+__device__ __forceinline__ uint32_t max_row16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, true));
+  return v;
+}
+
+// max |y| as an integer: the bits of nonnegative floats are in their order,
+// and a NaN's lie above infinity's, so a NaN is the largest.
+__device__ __forceinline__ uint32_t absmax8(const F8& y) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, fbits(y.v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+  const float s = bitsf(amax_bits) / 448.0f;
+  return s < kTiny ? kTiny : s;  // a NaN stays
+}
+
+__device__ __forceinline__ u32x2 codes8(const F8& y, float inv) {
+  F8 q;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q.v[i] = clampf(y.v[i] * inv, -448.f, 448.f);
+  return u32x2{e4m3_pack4(q.v[0], q.v[1], q.v[2], q.v[3]), e4m3_pack4(q.v[4], q.v[5], q.v[6], q.v[7])};
+}
+
+// ---------------------------------------------------------------- activation rows, gated activation
+// One lane per 8 elements, one 16-lane row per scale block; the blocks of all
+// rows are numbered through, so short rows share a workgroup.
+template <bool GATE>
+__global__ __launch_bounds__(256) void k_block_quant_rows(const uint16_t* __restrict__ X, int64_t ldx, uint32_t nblk,
+                                                          uint32_t KB, uint32_t K, uint8_t* __restrict__ Xq,
+                                                          float* __restrict__ Xs) {
+  const uint32_t blk = blockIdx.x * 16u + (threadIdx.x >> 4);
+  if (blk >= nblk) return;  // whole 16-lane rows leave together
+  const uint32_t m = blk / KB, k = (blk - m * KB) * 128u + (threadIdx.x & 15u) * 8u;
+  const bool in = k < K;  // K % 16 == 0: a lane's 8 elements are inside or outside together
+  F8 y{};
+  if (in) {
+    const uint16_t* p = X + (int64_t)m * ldx + k;
+    const F8 x = unpack8(*reinterpret_cast<const u32x4*>(p));
+    if constexpr (GATE) {
+      const F8 u = unpack8(*reinterpret_cast<const u32x4*>(p + K));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y.v[i] = x.v[i] / (1.0f + expf(-x.v[i])) * u.v[i];
+    } else {
+      y = x;
+    }
+  }
+  const float s = block_scale(max_row16(absmax8(y)));
+  if (in) {
+    *reinterpret_cast<u32x2*>(Xq + (int64_t)m * K + k) = codes8(y, 1.0f / s);
+    if ((threadIdx.x & 15u) == 0) Xs[blk] = s;
+  }
+}
+
+// ---------------------------------------------------------------- residual addition + RMS norm
+// A row belongs to WPR waves and stays in their registers from its one read to
+// its one write: lane l of wave w holds chunks w * 64 + l + 64 * WPR * j
+// (8 elements each) for j < CPT, so its 16-lane rows are scale blocks.  The
+// sum of squares crosses lanes by shuffles and waves through LDS.
+template <int WPR, int CPT>
+__global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void k_block_norm(BlockNormArgs a) {
+  constexpr int RPW = WPR >= 4 ? 1 : 4 / WPR;  // rows per workgroup
+  __shared__ float part[WPR >= 4 ? WPR : 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * RPW + wave / WPR;
+  const bool live = row < a.M;
+  const int64_t m = live ? row : 0;
+  const uint32_t K = (uint32_t)a.K, rb = live ? K * 2u : 0u;
+  const __amdgpu_buffer_rsrc_t Xr = make_rsrc(a.X + m * a.ldx, rb);
+  const __amdgpu_buffer_rsrc_t Rr = make_rsrc(a.residual ? a.residual + m * K : a.X, a.residual ? rb : 0u);
+  const __amdgpu_buffer_rsrc_t Gr = make_rsrc(a.gain, K * 2u);
+  const uint32_t c0 = (uint32_t)((wave % WPR) * 64 + lane);
+
+  u32x4 xw[CPT], rw[CPT], gw[CPT];
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) xw[j] = bload128(Xr, (c0 + 64u * WPR * j) * 16u);  // past the row: zeros
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) rw[j] = bload128(Rr, (c0 + 64u * WPR * j) * 16u);
+  }
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) gw[j] = bload128(Gr, (c0 + 64u * WPR * j) * 16u);
+
+  F8 h[CPT];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    h[j] = unpack8(xw[j]);
+    if (a.residual) {
+      const F8 r = unpack8(rw[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j].v[i] += r.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += h[j].v[i] * h[j].v[i];
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) ss += __shfl_xor(ss, d);
+  if constexpr (WPR > 1) {
+    if (lane == 0) part[wave] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) ss += part[wave / WPR * WPR + w];
+  }
+  const float rstd = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+
+  const uint32_t KB = (K + 127u) / 128u;
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const uint32_t c = c0 + 64u * WPR * j;
+    const bool in = live && c * 8u < K;
+    const F8 g = unpack8(gw[j]);
+    F8 y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y.v[i] = h[j].v[i] * rstd * g.v[i];
+    if (!in) y = F8{};  // a row of NaN or infinite rstd must not reach the tail lanes of its last block
+    const float s = block_scale(max_row16(absmax8(y)));
+    if (in) {
+      if (a.residual_out) *reinterpret_cast<u32x4*>(a.residual_out + m * K + c * 8u) = pack8(h[j]);
+      if (a.y_out) *reinterpret_cast<u32x4*>(a.y_out + m * K + c * 8u) = pack8(y);
+      *reinterpret_cast<u32x2*>(a.Xq + m * K + c * 8u) = codes8(y, 1.0f / s);
+      if ((lane & 15) == 0) a.Xs[m * KB + c / 16u] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- weights
+// One workgroup per 128 x 128 block: 16 lanes read a row of it, 16 rows at a
+// time.  Runs once per weight.
+__global__ __launch_bounds__(256) void k_block_quant_weight(const uint16_t* __restrict__ W, int N, int K,
+                                                            uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ uint32_t part[4];
+  const int kb = blockIdx.x, nb = blockIdx.y, KB = gridDim.x, NB = gridDim.y;
+  const int64_t base = (int64_t)blockIdx.z * N * K;
+  const int k = kb * 128 + (threadIdx.x & 15) * 8;
+  F8 y[8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int n = nb * 128 + 16 * j + (int)(threadIdx.x >> 4);
+    y[j] = F8{};
+    if (n < N && k < K) y[j] = unpack8(*reinterpret_cast<const u32x4*>(W + base + (int64_t)n * K + k));
+    amax = max(amax, absmax8(y[j]));
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = amax;
+  __syncthreads();
+  const float s = block_scale(max(max(part[0], part[1]), max(part[2], part[3])));
+  const float inv = 1.0f / s;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int n = nb * 128 + 16 * j + (int)(threadIdx.x >> 4);
+    if (n < N && k < K) *reinterpret_cast<u32x2*>(codes + base + (int64_t)n * K + k) = codes8(y[j], inv);
+  }
+  if (threadIdx.x == 0) scales[((int64_t)blockIdx.z * NB + nb) * KB + kb] = s;
+}
+
+}  // namespace
+
+hipError_t launch_block_quant_rows(bool gate, const uint16_t* X, int64_t ldx, int64_t M, int64_t K, uint8_t* Xq,
+                                   float* Xs, hipStream_t s) {
+  const uint32_t KB = (uint32_t)((K + 127) / 128), nblk = (uint32_t)M * KB;
+  const unsigned grid = (nblk + 15u) / 16u;
+  if (gate)
+    k_block_quant_rows<true><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, (uint32_t)K, Xq, Xs);
+  else
+    k_block_quant_rows<false><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, (uint32_t)K, Xq, Xs);
+  return hipGetLastError();
+}
+
+template <int WPR, int CPT>
+static void norm_launch(const BlockNormArgs& a, hipStream_t s) {
+  constexpr int rows = WPR >= 4 ? 1 : 4 / WPR;
+  k_block_norm<WPR, CPT><<<(unsigned)((a.M + rows - 1) / rows), WPR >= 4 ? WPR * 64 : 256, 0, s>>>(a);
+}
+
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
+  const int chunks = (a.K + 127) / 128 * 16;  // whole 16-lane rows
+  if (chunks <= 64) norm_launch<1, 1>(a, s);
+  else if (chunks <= 128) norm_launch<2, 1>(a, s);
+  else if (chunks <= 256) norm_launch<4, 1>(a, s);
+  else if (chunks <= 512) norm_launch<4, 2>(a, s);
+  else if (chunks <= 1024) norm_launch<4, 4>(a, s);
+  else if (chunks <= 2048) norm_launch<8, 4>(a, s);
+  else norm_launch<16, 4>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_block_quant_weight(const uint16_t* W, int64_t E, int64_t N, int64_t K, uint8_t* codes,
+                                     float* scales, hipStream_t s) {
+  const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128), (unsigned)E);
+  k_block_quant_weight<<<grid, 256, 0, s>>>(W, (int)N, (int)K, codes, scales);
+  return hipGetLastError();
+}
+
+}  // namespace wq
