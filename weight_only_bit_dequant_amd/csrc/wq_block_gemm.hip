@@ -18,9 +18,10 @@ typedef __attribute__((ext_vector_type(8))) int i32x8;
 constexpr uint32_t kOut = 0xFFFFFFF0u;  // at or past the end of every buffer here (sizes < 2^32, multiples of 16)
 
 // lane (g, c) of A: 32 codes of weight row c, of B: 32 codes of activation row
-// c, both at K 32g .. 32g+31; D[4g + r][c] in element r.  Unit block scales.
+// c, both at K 32g .. 32g+31; D[4g + r][c] in element r.  (Scale operands 0
+// select the instruction without block scales.)
 __device__ __forceinline__ f32x4 mfma_blk(i32x8 w, i32x8 x) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
@@ -103,9 +104,279 @@ __global__ __launch_bounds__(256) void k_block_direct(BlockGemmArgs a) {
     if (n + r < N) a.Y[(int64_t)m * N + n + r] = f32_to_bf16(acc[r] + (a.bias ? bf16_to_f32(a.bias[n + r]) : 0.f));
 }
 
+// ---------------------------------------------------------------- LDS-tiled kernel
+// A workgroup of WN x WM waves owns BN columns x BM rows of Y; K advances one
+// scale block (128) per step.  Operand rows go from memory straight into LDS
+// (buffer_load ... lds: lane i's 16 bytes land at the wave's base + 16 i), 8
+// whole rows of 128 bytes per instruction, NS stages deep, chunks of a row
+// XOR-swizzled by the choice of the chunk each lane reads (blk_pos).
+//
+// The products sa * sb of the tile's scales wait in LDS too, four steps at a
+// time ([buffer][128-column block][row][4]): the BM first threads load four
+// scales of one activation row at once, which costs a quarter of the line
+// requests of one load per step.
+//
+// Step: a wave holds its TM activation fragments and streams its TN weight
+// fragments, each meeting TM MFMAs while the VALU scales and adds the previous
+// fragment's results.  All LDS reads of a stage are done one fragment before
+// the step's end; there the waves meet at the step's one barrier, and the last
+// fragment's MFMAs cover the first reads of the next stage and the issue of
+// the loads that replace this one.
+constexpr int kScaleSteps = 4;
+
+// LDS slot of 16-byte chunk k of row r: the four lane groups' reads of 16 rows
+// then fall on distinct banks.
+__device__ __forceinline__ int blk_pos(int r, int k) { return k ^ (((r >> 1) & 1) | (r & 4)); }
+
+template <int BN, int BM, int WN, int WM, int NS>
+struct TileT {
+  static constexpr int WAVES = WN * WM, TN = BN / (16 * WN), TM = BM / (16 * WM);
+  static constexpr int STAGE = (BN + BM) * 128;
+  static constexpr int NB = BN / 128 ? BN / 128 : 1;  // 128-column blocks
+  static constexpr int SBUF = NB * BM * 4 * kScaleSteps;
+  static constexpr int PITCH = TN * 32 + 16;  // output tile row in LDS
+  static constexpr int OUT = WAVES * TM * 16 * PITCH;
+  static constexpr int MAIN = NS * STAGE + 2 * SBUF;
+  static constexpr int SMEM = MAIN > OUT ? MAIN : OUT;
+  static_assert(BM <= WAVES * 64, "a thread per row of scales");
+  static_assert(BN % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole loads of 8 rows");
+};
+
+template <int BN, int BM, int WN, int WM, int NS>
+__global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
+  using T = TileT<BN, BM, WN, WM, NS>;
+  constexpr int TN = T::TN, TM = T::TM, W = T::WAVES;
+  constexpr int LJW = BN / (8 * W), LJ = (BN + BM) / (8 * W);  // loads per wave and step: weights, all
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  float* sc = reinterpret_cast<float*>(smem + NS * T::STAGE);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int wn = wave % WN, wm = wave / WN;
+  const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
+
+  // XCD-aware tile order: workgroup b runs on XCD b % 8; each XCD takes a
+  // contiguous piece of an order that fills bands of 4 column tiles row tile
+  // by row tile, so tiles in flight on one L2 share operands both ways
+  int tx, ty;
+  {
+    const int G = gx * gy, b = blockIdx.x, q = G >> 3, r = G & 7, x = b & 7;
+    const int idx = x * q + min(x, r) + (b >> 3);
+    const int band = idx / (4 * gy), in = idx - band * 4 * gy, wide = min(4, gx - 4 * band);
+    ty = in / wide;
+    tx = 4 * band + in - ty * wide;
+  }
+  RowTile t{0, ty * BM, a.M};
+  if (a.offsets) {
+    t = row_tile(a.offsets, a.E, a.T, BM, ty);
+    if (t.e < 0) return;
+  }
+  const int n0 = tx * BN;
+
+  // load j of this wave: rows (j * W + wave) * 8 + lane / 8 of the stage, weights first; chunk kc of the row
+  const int lr = lane >> 3, kc16 = 16 * blk_pos(lr, lane & 7);
+  const __amdgpu_buffer_rsrc_t Wr =
+      make_rsrc(a.Wq + ((int64_t)t.e * N + n0) * K, (uint32_t)min(BN, N - n0) * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t Xr = a.rows ? make_rsrc(a.Xq, (uint32_t)((int64_t)a.M * K))
+                                           : make_rsrc(a.Xq + (int64_t)t.t0 * K, (uint32_t)min(BM, t.end - t.t0) * (uint32_t)K);
+  uint32_t voff[LJ];  // rows past the end repeat the last
+#pragma unroll
+  for (int j = 0; j < LJ; ++j) {
+    const int r = (j * W + wave) * 8 + lr;
+    voff[j] = (uint32_t)(j < LJW ? min(r, N - n0 - 1) : min(r - BN, t.end - t.t0 - 1));
+  }
+  const int srow = t.t0 + min(tid, t.end - t.t0 - 1);  // the row whose scales thread tid < BM stages
+  int ssrc = srow;
+  uint32_t limit = 0xFFFFFFFFu;  // source rows from here on read as zeros
+  if (a.rows) {
+    limit = (uint32_t)a.M;
+    ssrc = a.rows[srow];
+#pragma unroll
+    for (int j = LJW; j < LJ; ++j) voff[j] = (uint32_t)a.rows[t.t0 + voff[j]];
+  }
+#pragma unroll
+  for (int j = 0; j < LJ; ++j)
+    voff[j] = j < LJW || voff[j] < limit ? voff[j] * (uint32_t)K + kc16 : kOut;
+  auto issue = [&](int kt, int st) {
+    const bool ok = kt * 128 + kc16 < K;
+    const int soff = min(kt, KB - 1) * 128;
+#pragma unroll
+    for (int j = 0; j < LJ; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          j < LJW ? Wr : Xr, (__attribute__((address_space(3))) void*)(smem + st * T::STAGE + (j * W + wave) * 1024), 16,
+          (int)(ok ? voff[j] : kOut), soff, 0, 0);
+  };
+
+  // scales of steps [first(ch), first(ch) + 4): thread `tid` owns row tid
+  const float* sa = nullptr;  // its activation row's scales (null: a row without any)
+  if (tid < BM && (uint32_t)ssrc < (uint32_t)a.M) sa = a.Xs + (int64_t)ssrc * KB;
+  const float* sb = a.Ws + ((int64_t)t.e * NBLK + n0 / 128) * KB;
+  auto first = [&](int ch) { return max(0, min(kScaleSteps * ch, KB - kScaleSteps)); };
+  typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+  auto load4 = [&](const float* p) {
+    if (KB >= kScaleSteps) return f32x4(*reinterpret_cast<const f32x4u*>(p));
+    return f32x4{p[0], p[min(1, KB - 1)], p[min(2, KB - 1)], p[KB - 1]};
+  };
+  f32x4 sav, sbv[T::NB];
+  auto load_scales = [&](int ch) {
+    sav = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (sa) {
+      sav = load4(sa + first(ch));
+#pragma unroll
+      for (int q = 0; q < T::NB; ++q) sbv[q] = load4(sb + (int64_t)min(q, NBLK - 1 - n0 / 128) * KB + first(ch));
+    }
+  };
+  auto store_scales = [&](int ch) {
+    if (tid < BM) {
+#pragma unroll
+      for (int q = 0; q < T::NB; ++q)
+        *reinterpret_cast<f32x4*>(sc + ((ch & 1) * T::NB + q) * BM * kScaleSteps + tid * kScaleSteps) =
+            sa ? sav * sbv[q] : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+
+  // operand fragments: rows 16 i + c of the wave's part, K 32 g .. 32 g + 31 = chunks 2g, 2g + 1
+  const int flo = c * 128 + blk_pos(c, 2 * g) * 16;
+  const unsigned char* fw = smem + wn * TN * 2048;
+  const unsigned char* fx = smem + BN * 128 + wm * TM * 2048;
+  auto frag = [&](const unsigned char* base, int st, int i) {
+    const unsigned char* p = base + st * T::STAGE + i * 2048;
+    return join(*reinterpret_cast<const u32x4*>(p + flo), *reinterpret_cast<const u32x4*>(p + (flo ^ 16)));
+  };
+  const float* scw = sc + ((wn * TN * 16) / 128 * BM + wm * TM * 16 + c) * kScaleSteps;
+  auto scale = [&](int kt, int i) {
+    const int ch = kt / kScaleSteps;
+    return scw[(ch & 1) * T::NB * BM * kScaleSteps + i * 16 * kScaleSteps + kt - first(ch)];
+  };
+
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  load_scales(0);
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(st, st);
+  store_scales(0);
+  __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
+  asm volatile("s_barrier" ::: "memory");
+  issue(NS - 1, NS - 1);
+
+  i32x8 B[TM], A;
+  f32x4 p[2][TM];  // products of the fragment before the last, scaled while the last one's are made
+  float s[TM], sold[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    B[j] = frag(fx, 0, j);
+    sold[j] = s[j] = scale(0, j);
+    p[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  A = frag(fw, 0, 0);
+  static_assert(TN % 2 == 0, "the pair of product buffers alternates");
+  auto add = [&](int i, int j, const f32x4& v, float f) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], f, acc[i][j][r]);
+  };
+  int st = 0;
+  for (int kt = 0; kt < KB; ++kt) {
+    const int nst = st + 1 == NS ? 0 : st + 1;
+#pragma unroll
+    for (int i = 0; i < TN - 1; ++i) {
+      const i32x8 An = frag(fw, st, i + 1);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        p[i & 1][j] = mfma_blk(A, B[j]);
+        add(i ? i - 1 : TN - 1, j, p[(i & 1) ^ 1][j], i ? s[j] : sold[j]);
+      }
+      A = An;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // every read of this stage has been made: meet, then refill it
+    __builtin_amdgcn_s_waitcnt((kWaitVm0 & kWaitLgkm0) | ((NS - 2) * LJ & 15) | (((NS - 2) * LJ >> 4) << 14));
+    asm volatile("s_barrier" ::: "memory");
+    const int sub = kt & (kScaleSteps - 1);
+    if (sub == 0) load_scales(kt / kScaleSteps + 1);
+    if (sub == 2) store_scales(kt / kScaleSteps + 1);
+    if (NS > 2 || kt + NS < KB) issue(kt + NS, st);
+    const i32x8 An = frag(fw, nst, 0);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      p[1][j] = mfma_blk(A, B[j]);
+      add(TN - 2, j, p[0][j], s[j]);
+      sold[j] = s[j];
+      B[j] = frag(fx, nst, j);
+      s[j] = scale(min(kt + 1, KB - 1), j);
+    }
+    A = An;
+    __builtin_amdgcn_sched_barrier(0);
+    st = nst;
+  }
+#pragma unroll
+  for (int j = 0; j < TM; ++j) add(TN - 1, j, p[1][j], sold[j]);
+
+  // output: wave tiles leave through LDS as 16-byte row pieces
+  __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
+  asm volatile("s_barrier" ::: "memory");
+  unsigned char* et = smem + wave * (TM * 16 * T::PITCH);
+  const int nw = n0 + wn * TN * 16, mw = t.t0 + wm * TM * 16;
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.bias) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = bf16_to_f32(a.bias[min(nw + 16 * i + 4 * g + r, N - 1)]);
+    }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      u32x2 v;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[h] = (uint32_t)f32_to_bf16(acc[i][j][2 * h] + b[2 * h]) |
+               ((uint32_t)f32_to_bf16(acc[i][j][2 * h + 1] + b[2 * h + 1]) << 16);
+      *reinterpret_cast<u32x2*>(et + (16 * j + c) * T::PITCH + (16 * i + 4 * g) * 2) = v;
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+  asm volatile("" ::: "memory");
+  constexpr int LPR = TN * 2, RPI = 64 / LPR;  // lanes per row, rows per store instruction
+  const bool vec = (N & 7) == 0;
+#pragma unroll
+  for (int q = 0; q < TM * 16 / RPI; ++q) {
+    const int row = RPI * q + lane / LPR, col = 8 * (lane % LPR);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(et + row * T::PITCH + col * 2);
+    const int m = mw + row, n = nw + col;
+    if (m < t.end) {
+      uint16_t* y = a.Y + (int64_t)m * N + n;
+      if (vec) {
+        if (n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < N) y[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  }
+}
+
 }  // namespace
 
+template <int BN, int BM, int WN, int WM, int NS>
+static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
+  using T = TileT<BN, BM, WN, WM, NS>;
+  static std::atomic<int> allowed{0};
+  const auto kern = k_block_tile<BN, BM, WN, WM, NS>;
+  hipError_t e = allow_smem(kern, T::SMEM, allowed);
+  if (e != hipSuccess) return e;
+  const int64_t gx = (a.N + BN - 1) / BN;
+  const int64_t gy = a.offsets ? (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
+  kern<<<(unsigned)(gx * gy), WN * WM * 64, T::SMEM, s>>>(a, (int)gx, (int)gy);
+  return hipGetLastError();
+}
+
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
+  if (a.T >= 1024) return tile_launch<256, 256, 2, 4, 2>(a, s);
+  if (a.T >= 128) return tile_launch<128, 128, 2, 2, 2>(a, s);
   // row tiles of 16: every expert with rows may end in a partial one
   const int64_t tiles = a.offsets ? (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * 15) / 16 : (a.M + 15) / 16;
   k_block_direct<<<dim3((unsigned)((a.N + 63) / 64), (unsigned)tiles), 256, 0, s>>>(a);
