@@ -117,11 +117,11 @@ __global__ __launch_bounds__(256) void k_block_direct(BlockGemmArgs a) {
 // requests of one load per step.
 //
 // Step: a wave holds its TM activation fragments and streams its TN weight
-// fragments, each meeting TM MFMAs while the VALU scales and adds the previous
-// fragment's results.  All LDS reads of a stage are done one fragment before
-// the step's end; there the waves meet at the step's one barrier, and the last
-// fragment's MFMAs cover the first reads of the next stage and the issue of
-// the loads that replace this one.
+// fragments, read two fragments ahead; each meets TM MFMAs, and the VALU scales
+// and adds every result three MFMAs later.  All LDS reads of a stage are done two
+// fragments before the step's end; there the waves meet at the step's one
+// barrier, and the last two fragments' MFMAs cover the first reads of the next
+// stage.
 constexpr int kScaleSteps = 4;
 
 // LDS slot of 16-byte chunk k of row r: the four lane groups' reads of 16 rows
@@ -197,14 +197,10 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, 
 #pragma unroll
   for (int j = 0; j < LJ; ++j)
     voff[j] = j < LJW || voff[j] < limit ? voff[j] * (uint32_t)K + kc16 : kOut;
-  auto issue = [&](int kt, int st) {
-    const bool ok = kt * 128 + kc16 < K;
-    const int soff = min(kt, KB - 1) * 128;
-#pragma unroll
-    for (int j = 0; j < LJ; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          j < LJW ? Wr : Xr, (__attribute__((address_space(3))) void*)(smem + st * T::STAGE + (j * W + wave) * 1024), 16,
-          (int)(ok ? voff[j] : kOut), soff, 0, 0);
+  auto issue1 = [&](int kt, int st, int j) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        j < LJW ? Wr : Xr, (__attribute__((address_space(3))) void*)(smem + st * T::STAGE + (j * W + wave) * 1024), 16,
+        (int)(kt * 128 + kc16 < K ? voff[j] : kOut), min(kt, KB - 1) * 128, 0, 0);
   };
 
   // scales of steps [first(ch), first(ch) + 4): thread `tid` owns row tid
@@ -257,63 +253,85 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, 
 
   load_scales(0);
 #pragma unroll
-  for (int st = 0; st < NS - 1; ++st) issue(st, st);
+  for (int st = 0; st < NS - 1; ++st)
+#pragma unroll
+    for (int j = 0; j < LJ; ++j) issue1(st, st, j);
   store_scales(0);
   __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
   asm volatile("s_barrier" ::: "memory");
-  issue(NS - 1, NS - 1);
+  // A freed stage's loads are spread over SPAN fragments' MFMAs (two of the
+  // step that frees it, the rest of the next one): issued in one go they fill
+  // the memory pipe's queue and the waves stall on it.
+  constexpr int SPAN = TN >= 8 ? TN - 2 : TN - 1;
+  auto slot = [](int l) { return l * SPAN / LJ; };
+#pragma unroll
+  for (int l = 0; l < LJ; ++l)
+    if (slot(l) < 2) issue1(NS - 1, NS - 1, l);
 
-  i32x8 B[TM], A;
-  f32x4 p[2][TM];  // products of the fragment before the last, scaled while the last one's are made
-  float s[TM], sold[TM];
+  // ring of weight fragments: fragment i in slot i % R, so that the next step's
+  // first two find slots 0 and 1 free at the end of this step
+  constexpr int R = TN % 3 == 2 ? 3 : 4;
+  static_assert(TN % R == 2 || TN % R == 0, "slots 0 and 1 are free in time");
+  i32x8 A[R], B[TM];
+  // products, scaled and added LAG MFMAs after they were made: fewer, and the VALU would wait for their results
+  constexpr int LAG = 3;
+  f32x4 p[LAG + 1];
+  float s[TM];
+  A[0] = frag(fw, 0, 0);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     B[j] = frag(fx, 0, j);
-    sold[j] = s[j] = scale(0, j);
-    p[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s[j] = scale(0, j);
   }
-  A = frag(fw, 0, 0);
-  static_assert(TN % 2 == 0, "the pair of product buffers alternates");
-  auto add = [&](int i, int j, const f32x4& v, float f) {
+  A[1] = frag(fw, 0, 1);
+  auto add = [&](int q) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], f, acc[i][j][r]);
+    for (int r = 0; r < 4; ++r)
+      acc[q / TM][q % TM][r] = __builtin_fmaf(p[q % (LAG + 1)][r], s[q % TM], acc[q / TM][q % TM][r]);
   };
-  int st = 0;
-  for (int kt = 0; kt < KB; ++kt) {
-    const int nst = st + 1 == NS ? 0 : st + 1;
+  // one step; `pst`, `st`, `nst`: the stages of the last, this and the next one
+  auto step = [&](int kt, int pst, int st, int nst) {
+    constexpr int Q = TN * TM, MEET = (TN - 2) * TM;
 #pragma unroll
-    for (int i = 0; i < TN - 1; ++i) {
-      const i32x8 An = frag(fw, st, i + 1);
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        p[i & 1][j] = mfma_blk(A, B[j]);
-        add(i ? i - 1 : TN - 1, j, p[(i & 1) ^ 1][j], i ? s[j] : sold[j]);
+    for (int q = 0; q < Q; ++q) {
+      const int i = q / TM, j = q % TM;
+      if (j == 0 && i + 2 < TN) A[(i + 2) % R] = frag(fw, st, i + 2);
+      if (q == MEET) {
+        // every read of this stage has been made: meet, then refill it
+        __builtin_amdgcn_s_waitcnt((kWaitVm0 & kWaitLgkm0) | ((NS - 2) * LJ & 15) | (((NS - 2) * LJ >> 4) << 14));
+        asm volatile("s_barrier" ::: "memory");
+        const int sub = kt & (kScaleSteps - 1);
+        if (sub == 0) load_scales(kt / kScaleSteps + 1);
+        if (sub == 2) store_scales(kt / kScaleSteps + 1);
       }
-      A = An;
+      p[q % (LAG + 1)] = mfma_blk(A[i % R], B[j]);
+      if (q >= LAG) add(q - LAG);
+#pragma unroll
+      for (int l = 0; l < LJ; ++l) {
+        // in a slot's first MFMAs, one load each
+        const int at = slot(l), nth = l - (at * LJ + SPAN - 1) / SPAN;
+        if (j == min(nth, TM - 1)) {
+          if (at < 2 && i == TN - 2 + at) issue1(kt + NS, st, l);
+          if (at >= 2 && i == at - 2) issue1(kt + NS - 1, pst, l);
+        }
+      }
+      if (q == MEET + TM - 1) A[0] = frag(fw, nst, 0);
+      if (i == TN - 1) B[j] = frag(fx, nst, j);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // every read of this stage has been made: meet, then refill it
-    __builtin_amdgcn_s_waitcnt((kWaitVm0 & kWaitLgkm0) | ((NS - 2) * LJ & 15) | (((NS - 2) * LJ >> 4) << 14));
-    asm volatile("s_barrier" ::: "memory");
-    const int sub = kt & (kScaleSteps - 1);
-    if (sub == 0) load_scales(kt / kScaleSteps + 1);
-    if (sub == 2) store_scales(kt / kScaleSteps + 1);
-    if (NS > 2 || kt + NS < KB) issue(kt + NS, st);
-    const i32x8 An = frag(fw, nst, 0);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      p[1][j] = mfma_blk(A, B[j]);
-      add(TN - 2, j, p[0][j], s[j]);
-      sold[j] = s[j];
-      B[j] = frag(fx, nst, j);
-      s[j] = scale(min(kt + 1, KB - 1), j);
-    }
-    A = An;
+    for (int q = Q - LAG; q < Q; ++q) add(q);
+    A[1] = frag(fw, nst, 1);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) s[j] = scale(min(kt + 1, KB - 1), j);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int kt = 0, pst = NS - 1, st = 0; kt < KB; ++kt) {
+    const int nst = st + 1 == NS ? 0 : st + 1;
+    step(kt, pst, st, nst);
+    pst = st;
     st = nst;
   }
-#pragma unroll
-  for (int j = 0; j < TM; ++j) add(TN - 1, j, p[1][j], sold[j]);
 
   // output: wave tiles leave through LDS as 16-byte row pieces
   __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
