@@ -20,8 +20,8 @@
  * Conventions are those of wq.h: device pointers owned by the caller, row-major
  * tensors, bf16 as uint16 bit patterns, stream-ordered calls that neither wait
  * nor allocate, every check on the host before anything is enqueued,
- * wq_last_error() for the reason.  Base pointers of codes, bf16 tensors and
- * workspaces must be 16-byte aligned, the other pointers aligned to their type.
+ * wq_last_error() for the reason.  Base pointers of codes and bf16 tensors
+ * must be 16-byte aligned (a bias 2-byte), the other pointers aligned to their type.
  * K % 16 == 0 everywhere (WQ_ESHAPE otherwise).
  */
 #ifndef WQ_BLOCK_H
@@ -82,13 +82,10 @@ wq_status wq_block_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int
  *   Y[m][n] = bf16( sum_kb Xs[m][kb] Ws[n / 128][kb] sum_{k in kb} Xq[m][k] Wq[n][k] (+ bias[n]) )
  * Each block's products are summed by the FP8 matrix cores in fp32, scaled and
  * added to an fp32 sum; one rounding to bf16.  bias: bf16 [N] or NULL.  Any M
- * and N.  Workspace: wq_block_linear_workspace bytes (0 for most shapes), no
- * initialisation; calls that may overlap need different ones.
+ * and N.  No workspace.
  */
-size_t wq_block_linear_workspace(int64_t M, int64_t N, int64_t K);
 wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const void* Wq, const float* Ws,
-                          const void* bias, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
-                          void* stream);
+                          const void* bias, int64_t N, void* Y, void* stream);
 
 /*
  * The same product for E experts over rows sorted by expert:

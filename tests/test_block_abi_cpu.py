@@ -22,7 +22,7 @@ V = ctypes.c_void_p
 def test_every_declared_symbol_is_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(wq_block_[a-z0-9_]+)\s*\(", text)))
-    assert len(names) == 7
+    assert len(names) == 6
     for n in names:
         assert hasattr(block._lib(), n), n
 
@@ -44,7 +44,7 @@ def weight(W=16, E=1, N=4, K=144, C=16, S=4):
 
 
 def linear(X=16, Xs=4, M=4, K=144, W=16, Ws=4, B=2, N=24, Y=16):
-    return block._lib().wq_block_linear(V(X), V(Xs), M, K, V(W), V(Ws), V(B), N, V(Y), None, 0, None)
+    return block._lib().wq_block_linear(V(X), V(Xs), M, K, V(W), V(Ws), V(B), N, V(Y), None)
 
 
 def grouped(X=16, Xs=4, M=4, K=144, R=4, O=4, T=8, E=3, W=16, Ws=4, N=24, Y=16):

@@ -11,10 +11,11 @@ part, from the residual stream to the experts' outputs:
   grouped_linear         the same for rows sorted by expert, ragged counts
 
 and ``quantize_weight`` for the weights, which is done once.  As in ``wq``,
-each function checks what the C side cannot see (types, shapes, strides,
-devices), allocates the outputs that were not passed in, and forwards device
-pointers and torch's current stream; all compute runs in libwq.so and there is
-no fallback path.  Tensors of other types, shapes, strides or devices than
+each function allocates the outputs that were not passed in, checks what the C
+ABI cannot see (types, shapes, strides, devices) and forwards device pointers
+and torch's current stream; all compute runs in libwq.so and there is no
+fallback path.  The checks and the call are compiled (csrc/wq_block_py.cpp):
+a decode step's kernels are shorter than the same checks in Python.  Tensors of other types, shapes, strides or devices than
 stated raise; nothing is converted or copied silently.
 """
 
@@ -26,28 +27,39 @@ from . import wq
 
 BLOCK = 128
 
-_U8, _F32, _BF16, _I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
-_stream_of = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_U8, _F32, _BF16 = torch.uint8, torch.float32, torch.bfloat16
 
 _L = None
+_C = None  # the compiled entry points (csrc/wq_block_py.cpp), bound to the loaded library
 
 
 def _lib():
+    """The C functions by ctypes (``quantize_weight`` and tests)."""
     global _L
     if _L is None:
         L = wq.lib()
-        P, I64, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        P, I64, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
         L.wq_block_quantize_weight.argtypes = [P, I64, I64, I64, P, P, P]
         L.wq_block_quantize_act.argtypes = [P, I64, I64, I64, P, P, P]
         L.wq_block_silu_mul_quantize.argtypes = [P, I64, I64, I64, P, P, P]
         L.wq_block_add_rmsnorm_quantize.argtypes = [P, I64, P, P, F, I64, I64, P, P, P, P, P]
-        L.wq_block_linear_workspace.argtypes = [I64, I64, I64]
-        L.wq_block_linear_workspace.restype = SZ
-        L.wq_block_linear.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, SZ, P]
+        L.wq_block_linear.argtypes = [P, P, I64, I64, P, P, P, I64, P, P]
         L.wq_block_grouped_linear.argtypes = [P, P, I64, I64, P, P, I64, I64, P, P, I64, P, P]
         _L = L
     return _L
+
+
+def _calls():
+    global _C
+    if _C is None:
+        L = _lib()
+        from . import _block_call  # raises if it has not been built
+
+        _block_call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.wq_block_quantize_act, L.wq_block_silu_mul_quantize, L.wq_block_add_rmsnorm_quantize,
+            L.wq_block_linear, L.wq_block_grouped_linear)])
+        _C = _block_call
+    return _C
 
 
 def blocks(n):
@@ -60,47 +72,14 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _tensor(t, name, dtype, shape, device):
-    """`t` is a contiguous tensor of this type and shape on `device`."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s, strides %s, on %s)" % (
-            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.stride(), t.device))
-    return t
+def _matrix(t, name):
+    _need(isinstance(t, torch.Tensor) and t.dim() == 2, "%s must be a matrix" % name)
+    return t.shape
 
 
-def _rows(t, name, dtype):
-    """`t` is a GPU matrix whose rows are contiguous; returns (M, K, row stride)."""
-    if t.dtype is not dtype or t.dim() != 2 or not t.is_cuda:
-        raise ValueError("%s must be a %s matrix on the GPU (got %s of shape %s on %s)" % (
-            name, dtype, t.dtype, tuple(t.shape), t.device))
-    M, K = t.shape
-    ld, one = t.stride()
-    if M == 1:
-        ld = K  # a single row's stride says nothing
-    _need(one == 1 or K == 1, "%s must have contiguous rows (strides %s)" % (name, t.stride()))
-    return M, K, ld
-
-
-def _call(fn, name, device, *args):
-    """Enqueue on `device`'s current stream."""
-    index = device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return wq._check(fn(*args, _stream_of(index)), name)
-    status = fn(*args, _stream_of(index))
-    if status:
-        wq._check(status, name)
-
-
-def _codes(out, M, K, device):
-    """The (codes, scales) output buffers of a quantizing operator."""
-    if out is None:
-        return (torch.empty((M, K), dtype=_U8, device=device),
-                torch.empty((M, blocks(K)), dtype=_F32, device=device))
-    xq, xs = out
-    _tensor(xq, "codes", _U8, (M, K), device)
-    _tensor(xs, "scales", _F32, (M, blocks(K)), device)
-    return xq, xs
+def _codes(M, K, device):
+    """New (codes, scales) buffers of a quantizing operator."""
+    return (torch.empty((M, K), dtype=_U8, device=device), torch.empty((M, blocks(K)), dtype=_F32, device=device))
 
 
 # ---------------------------------------------------------------- quantizers
@@ -112,36 +91,40 @@ def quantize_weight(W):
     Returns the weight dict that ``linear`` (or ``grouped_linear``) takes:
     ``codes`` uint8 of W's shape, ``scales`` float32 [(E,) ceil(N/128),
     ceil(K/128)], and the sizes ``E``, ``N``, ``K``."""
-    _need(W.dim() in (2, 3) and W.dtype is _BF16 and W.is_cuda, "W must be a bf16 tensor [N, K] or [E, N, K] on the GPU")
+    _need(W.dim() in (2, 3) and W.dtype is _BF16 and W.is_cuda and W.is_contiguous(),
+          "W must be a contiguous bf16 tensor [N, K] or [E, N, K] on the GPU")
     N, K = W.shape[-2:]
     E = 1 if W.dim() == 2 else W.shape[0]
-    _tensor(W, "W", _BF16, W.shape, W.device)
     codes = torch.empty(W.shape, dtype=_U8, device=W.device)
     scales = torch.empty(tuple(W.shape[:-2]) + (blocks(N), blocks(K)), dtype=_F32, device=W.device)
-    _call(_lib().wq_block_quantize_weight, "wq_block_quantize_weight", W.device,
-          W.data_ptr(), E, N, K, codes.data_ptr(), scales.data_ptr())
+    with torch.cuda.device(W.device):
+        wq._check(_lib().wq_block_quantize_weight(W.data_ptr(), E, N, K, codes.data_ptr(), scales.data_ptr(),
+                                                  wq._stream(W.device)), "wq_block_quantize_weight")
     return {"E": E, "N": N, "K": K, "codes": codes, "scales": scales}
 
 
 def quantize_act(X, out=None):
     """Quantize bf16 rows X[M, K] -> (codes uint8 [M, K], scales float32
     [M, ceil(K/128)]).  Rows may be strided (a multiple of 8 elements)."""
-    M, K, ld = _rows(X, "X", _BF16)
-    xq, xs = _codes(out, M, K, X.device)
-    _call(_lib().wq_block_quantize_act, "wq_block_quantize_act", X.device,
-          X.data_ptr(), ld, M, K, xq.data_ptr(), xs.data_ptr())
+    if out is None:
+        out = _codes(*_matrix(X, "X"), X.device)
+    xq, xs = out
+    status = _calls().quantize_act(X, xq, xs)
+    if status:
+        wq._check(status, "wq_block_quantize_act")
     return xq, xs
 
 
 def silu_mul_quantize(GU, out=None):
     """silu(gate) * up of GU[M, 2 K] = [gate | up], quantized -> (codes
     [M, K], scales).  Rows may be strided (a multiple of 8 elements)."""
-    M, K2, ld = _rows(GU, "GU", _BF16)
-    _need(K2 % 2 == 0, "GU must have an even number of columns (got %d)" % K2)
-    K = K2 // 2
-    xq, xs = _codes(out, M, K, GU.device)
-    _call(_lib().wq_block_silu_mul_quantize, "wq_block_silu_mul_quantize", GU.device,
-          GU.data_ptr(), ld, M, K, xq.data_ptr(), xs.data_ptr())
+    if out is None:
+        M, K2 = _matrix(GU, "GU")
+        out = _codes(M, K2 // 2, GU.device)
+    xq, xs = out
+    status = _calls().silu_mul_quantize(GU, xq, xs)
+    if status:
+        wq._check(status, "wq_block_silu_mul_quantize")
     return xq, xs
 
 
@@ -153,21 +136,14 @@ def add_rmsnorm_quantize(X, gain, eps=1e-5, residual=None, out=None, residual_ou
     y_out).  residual_out receives bf16(h): with a residual it is allocated
     unless passed in (it may be ``residual`` itself); without one it is None
     unless passed in.  y_out receives bf16(y) where it is passed in."""
-    M, K, ld = _rows(X, "X", _BF16)
-    dev = X.device
-    _tensor(gain, "gain", _BF16, (K,), dev)
-    xq, xs = _codes(out, M, K, dev)
-    r = ro = yo = None
-    if residual is not None:
-        r = _tensor(residual, "residual", _BF16, (M, K), dev).data_ptr()
-        if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=_BF16, device=dev)
-    if residual_out is not None:
-        ro = _tensor(residual_out, "residual_out", _BF16, (M, K), dev).data_ptr()
-    if y_out is not None:
-        yo = _tensor(y_out, "y_out", _BF16, (M, K), dev).data_ptr()
-    _call(_lib().wq_block_add_rmsnorm_quantize, "wq_block_add_rmsnorm_quantize", dev,
-          X.data_ptr(), ld, r, gain.data_ptr(), eps, M, K, xq.data_ptr(), xs.data_ptr(), ro, yo)
+    if out is None:
+        out = _codes(*_matrix(X, "X"), X.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(_matrix(X, "X"), dtype=_BF16, device=X.device)
+    xq, xs = out
+    status = _calls().add_rmsnorm_quantize(X, gain, eps, residual, xq, xs, residual_out, y_out)
+    if status:
+        wq._check(status, "wq_block_add_rmsnorm_quantize")
     return xq, xs, residual_out, y_out
 
 
@@ -180,23 +156,12 @@ def linear(Xq, Xs, q, bias=None, out=None):
     Xq uint8 [M, K] and Xs float32 [M, ceil(K/128)] from any quantizing
     operator above, q a ``quantize_weight`` result of one [N, K] weight, bias
     bf16 [N] or None."""
-    W, Ws = q["codes"], q["scales"]
-    dev = W.device
-    N, K = W.shape
-    M = Xq.shape[0]
-    _tensor(Xq, "Xq", _U8, (M, K), dev)
-    _tensor(Xs, "Xs", _F32, (M, blocks(K)), dev)
-    _weight(q, (N, K), (blocks(N), blocks(K)))
-    b = None if bias is None else _tensor(bias, "bias", _BF16, (N,), dev).data_ptr()
+    W = q["codes"]
     if out is None:
-        out = torch.empty((M, N), dtype=_BF16, device=dev)
-    else:
-        _tensor(out, "out", _BF16, (M, N), dev)
-    L = _lib()
-    need = L.wq_block_linear_workspace(M, N, K)
-    ws = wq.workspace(need, dev).data_ptr() if need else None
-    _call(L.wq_block_linear, "wq_block_linear", dev, Xq.data_ptr(), Xs.data_ptr(), M, K, W.data_ptr(),
-          Ws.data_ptr(), b, N, out.data_ptr(), ws, need)
+        out = torch.empty((_matrix(Xq, "Xq")[0], W.shape[0]), dtype=_BF16, device=W.device)
+    status = _calls().linear(Xq, Xs, W, q["scales"], bias, out)
+    if status:
+        wq._check(status, "wq_block_linear")
     return out
 
 
@@ -208,28 +173,12 @@ def grouped_linear(Xq, Xs, q, offsets, rows=None, out=None):
     row of each sorted row) or None (sorted row t is X's row t).  Rows of the
     output from offsets[E] on are not written.  Nothing is read back to the
     host, so the call can be captured in a graph."""
-    W, Ws = q["codes"], q["scales"]
-    dev = W.device
-    _need(W.dim() == 3, "grouped_linear takes stacked weights [E, N, K]")
-    E, N, K = W.shape
-    M = Xq.shape[0]
-    _tensor(Xq, "Xq", _U8, (M, K), dev)
-    _tensor(Xs, "Xs", _F32, (M, blocks(K)), dev)
-    _weight(q, (E, N, K), (E, blocks(N), blocks(K)))
-    _tensor(offsets, "offsets", _I32, (E + 1,), dev)
-    T = M if rows is None else rows.numel()
-    r = None if rows is None else _tensor(rows, "rows", _I32, (T,), dev).data_ptr()
+    W = q["codes"]
     if out is None:
-        out = torch.empty((T, N), dtype=_BF16, device=dev)
-    else:
-        _tensor(out, "out", _BF16, (T, N), dev)
-    _call(_lib().wq_block_grouped_linear, "wq_block_grouped_linear", dev, Xq.data_ptr(), Xs.data_ptr(), M, K, r,
-          offsets.data_ptr(), T, E, W.data_ptr(), Ws.data_ptr(), N, out.data_ptr())
+        _need(W.dim() == 3, "grouped_linear takes stacked weights [E, N, K]")
+        T = _matrix(Xq, "Xq")[0] if rows is None else rows.numel()
+        out = torch.empty((T, W.shape[1]), dtype=_BF16, device=W.device)
+    status = _calls().grouped_linear(Xq, Xs, W, q["scales"], offsets, rows, out)
+    if status:
+        wq._check(status, "wq_block_grouped_linear")
     return out
-
-
-def _weight(q, shape, scale_shape):
-    W, Ws = q["codes"], q["scales"]
-    _need(W.is_cuda, "the weight must be on the GPU")
-    _tensor(W, "weight codes", _U8, shape, W.device)
-    _tensor(Ws, "weight scales", _F32, scale_shape, W.device)

@@ -140,24 +140,13 @@ wq_status wq_block_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* 
   return launched(wq::launch_block_norm(a, (hipStream_t)stream), what);
 }
 
-size_t wq_block_linear_workspace(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
-}
-
 wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const void* Wq, const float* Ws,
-                          const void* bias, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
-                          void* stream) {
+                          const void* bias, int64_t N, void* Y, void* stream) {
   const char* what = "wq_block_linear";
   bool empty;
   wq_status st = check_gemm(what, Xq, Xs, M, K, Wq, Ws, N, 1, Y, M, &empty);
   if (st != WQ_OK || empty) return st;
   if (!aligned(bias, 2)) return fail(WQ_EALIGN, "%s: bias must be 2-byte aligned", what);
-  const size_t need = wq_block_linear_workspace(M, N, K);
-  if (need && (!workspace || workspace_bytes < need))
-    return fail(WQ_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given", what, need, workspace ? workspace_bytes : 0);
   wq::BlockGemmArgs a{};
   a.Xq = (const uint8_t*)Xq;
   a.Xs = Xs;
