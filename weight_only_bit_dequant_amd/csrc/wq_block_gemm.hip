@@ -28,6 +28,35 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// CH scales from p on (4-byte aligned); with fewer than CH blocks in a row
+// (KB < CH, p the row's start) the last one again.
+template <int CH>
+struct Scales {
+  float v[CH];
+};
+template <int CH>
+__device__ __forceinline__ Scales<CH> load_scales(const float* p, int KB) {
+  typedef float vec __attribute__((ext_vector_type(CH)));
+  typedef float vecu __attribute__((ext_vector_type(CH), aligned(4)));
+  Scales<CH> s;
+  if (KB >= CH) {
+    const vec v = *reinterpret_cast<const vecu*>(p);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) s.v[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) s.v[i] = p[min(i, KB - 1)];
+  }
+  return s;
+}
+
+// Place of this workgroup in an order that the XCDs share out in contiguous
+// pieces (workgroup b runs on XCD b % 8, and each XCD has its own L2).
+__device__ __forceinline__ int xcd_order(int G) {
+  const int b = blockIdx.x, q = G >> 3, r = G & 7, x = b & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
 // Row tile `ti` of the experts' row tiles, BM rows each, numbered through all
 // experts: expert e (-1: no such tile), its rows [t0, end).  Offsets are
 // clamped to [0, T].  Every lane of the wave gets the same answer.
@@ -63,45 +92,175 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* off, int E, int T, in
   return {-1, 0, 0};
 }
 
-// ---------------------------------------------------------------- direct kernel
-// 4 waves x 16 columns, 16 rows, all of K; operands straight from memory.
-__global__ __launch_bounds__(256) void k_block_direct(BlockGemmArgs a) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int N = a.N, K = a.K, KB = (K + 127) / 128, NB = (N + 127) / 128;
-  RowTile t = a.offsets ? row_tile(a.offsets, a.E, a.T, 16, blockIdx.y)
-                        : RowTile{0, (int)blockIdx.y * 16, a.M};
-  if (t.e < 0) return;
-  const int n0 = blockIdx.x * 64 + wave * 16;
-  if (n0 >= N) return;
-  const uint8_t* W = a.Wq + ((int64_t)t.e * N + n0) * K;
-  const float* Ws = a.Ws + ((int64_t)t.e * NB + n0 / 128) * KB;
-  const int m = t.t0 + c;
-  const bool mok = m < t.end;
-  const int src = mok ? (a.rows ? a.rows[m] : m) : 0;
-  const bool sok = mok && (uint32_t)src < (uint32_t)a.M;
-  const uint8_t* X = a.Xq + (int64_t)(sok ? src : 0) * K;
-  const float* Xs = a.Xs + (int64_t)(sok ? src : 0) * KB;
-  const bool nok = n0 + c < N;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < KB; ++kb) {
-    u32x4 w[2] = {}, x[2] = {};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * 128 + 32 * g + 16 * h;
-      if (k < K && nok) w[h] = *reinterpret_cast<const u32x4*>(W + (int64_t)c * K + k);
-      if (k < K && sok) x[h] = *reinterpret_cast<const u32x4*>(X + k);
-    }
-    const float s = (sok ? Xs[kb] : 0.f) * Ws[kb];
-    const f32x4 p = mfma_blk(join(w[0], w[1]), join(x[0], x[1]));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(p[r], s, acc[r]);
+// LDS slot of 16-byte chunk k of row r: the four lane groups' reads of 16 rows
+// then fall on distinct banks.
+__device__ __forceinline__ int blk_pos(int r, int k) { return k ^ (((r >> 1) & 1) | (r & 4)); }
+
+// ---------------------------------------------------------------- few rows: weight stream
+// A workgroup owns 16 NT columns x 16 MT rows and all of K; its W waves split
+// K, each a run of scale blocks.  A wave copies a block's rows into a slot of
+// its own in LDS (buffer_load ... lds, 8 whole 128-byte rows per instruction)
+// and reads them back as operands: loaded as operands, 16 rows of 64 bytes per
+// instruction, rows a power of two apart took twice as long (16 x 512 x 8192:
+// 11.3 against 4.9 us).  Waves meet once, to add up their sums.  One slot per
+// wave and more workgroups on a CU did as well as two or three slots (32 x 4096
+// x 3072 5.4-5.9 us either way; 64 rows of 32 experts, 2048 x 2048: 17 against
+// 15-17 us).  What bounds it is the weights' stream and, below some 10 MB, the
+// trips to memory.
+constexpr int kRun = 8;  // blocks whose scales a wave holds at a time
+
+template <int NT, int MT, int W>
+struct StreamT {
+  static constexpr int SLOT = (NT + MT) * 2048, L = 2 * (NT + MT);  // bytes and loads per block
+  static constexpr int PART = W * 16 * MT * 16 * NT * 4;
+  static constexpr int SMEM = W * SLOT > PART ? W * SLOT : PART;
+};
+
+template <int NT, int MT, int W>
+__global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx, int gy) {
+  using S = StreamT<NT, MT, W>;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
+  // consecutive workgroups of an XCD take the row tiles of one column tile, which share its weights
+  const int tile = xcd_order(gx * gy), tx = tile / gy, ty = tile - tx * gy;
+  RowTile t{0, ty * 16 * MT, a.M};
+  if (a.offsets) {
+    t = row_tile(a.offsets, a.E, a.T, 16 * MT, ty);
+    if (t.e < 0) return;
   }
-  if (!mok) return;
-  const int n = n0 + 4 * g;
+  const int n0 = tx * 16 * NT;
+
+  const __amdgpu_buffer_rsrc_t Wr =
+      make_rsrc(a.Wq + ((int64_t)t.e * N + n0) * K, (uint32_t)min(16 * NT, N - n0) * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t Xr = a.rows ? make_rsrc(a.Xq, (uint32_t)((int64_t)a.M * K))
+                                           : make_rsrc(a.Xq + (int64_t)t.t0 * K, (uint32_t)min(16 * MT, t.end - t.t0) * (uint32_t)K);
+  // load l of a block: rows 8 l + lane / 8 (weights first), chunk kc16 / 16 of the row; rows past the end read zeros
+  const int lr = lane >> 3, kc16 = 16 * blk_pos(lr, lane & 7);
+  uint32_t voff[S::L];
+  int src[MT];  // source row of operand row 16 j + c, -1: none
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (n + r < N) a.Y[(int64_t)m * N + n + r] = f32_to_bf16(acc[r] + (a.bias ? bf16_to_f32(a.bias[n + r]) : 0.f));
+  for (int j = 0; j < MT; ++j) {
+    const int m = t.t0 + 16 * j + c;
+    src[j] = m < t.end ? m : -1;
+  }
+#pragma unroll
+  for (int l = 0; l < S::L; ++l) {
+    const int r = 8 * l + lr;
+    voff[l] = (uint32_t)(l < 2 * NT ? (n0 + r < N ? r : -1) : (t.t0 + r - 16 * NT < t.end ? r - 16 * NT : -1));
+  }
+  uint32_t limit = 0x7FFFFFFFu;  // source rows from here on read as zeros
+  if (a.rows) {
+    limit = (uint32_t)a.M;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      if (src[j] >= 0) src[j] = a.rows[src[j]];
+#pragma unroll
+    for (int l = 2 * NT; l < S::L; ++l)
+      if ((int)voff[l] >= 0) voff[l] = (uint32_t)a.rows[t.t0 + voff[l]];
+  }
+#pragma unroll
+  for (int l = 0; l < S::L; ++l)
+    voff[l] = voff[l] < (l < 2 * NT ? 0x7FFFFFFFu : limit) ? voff[l] * (uint32_t)K + kc16 : kOut;
+  const float* sa[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) sa[j] = a.Xs + (int64_t)((uint32_t)src[j] < (uint32_t)a.M ? src[j] : 0) * KB;
+  const float* sb = a.Ws + ((int64_t)t.e * NBLK + n0 / 128) * KB;  // 16 NT columns lie in one block
+
+  unsigned char* slot = smem + wave * S::SLOT;
+  auto issue = [&](int kt) {
+#pragma unroll
+    for (int l = 0; l < S::L; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(l < 2 * NT ? Wr : Xr,
+                                               (__attribute__((address_space(3))) void*)(slot + l * 1024), 16,
+                                               (int)(kt * 128 + kc16 < K ? voff[l] : kOut), kt * 128, 0, 0);
+  };
+  const int flo = c * 128 + blk_pos(c, 2 * g) * 16;
+  auto frag = [&](int i) {
+    const unsigned char* p = slot + i * 2048;
+    return join(*reinterpret_cast<const u32x4*>(p + flo), *reinterpret_cast<const u32x4*>(p + (flo ^ 16)));
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int per = (KB + W - 1) / W, end = min(KB, (wave + 1) * per);
+  for (int k0 = wave * per; k0 < end; k0 += kRun) {
+    const int n = min(kRun, end - k0);
+    issue(k0);
+    // scales of kRun blocks from `first` on, so that none is read past the row; block k0 + u is number u + back
+    const int first = max(0, min(k0, KB - kRun)), back = k0 - first;
+    const Scales<kRun> bv = load_scales<kRun>(sb + first, KB);
+    Scales<kRun> av[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      av[j] = load_scales<kRun>(sa[j] + first, KB);
+#pragma unroll
+      for (int u = 0; u < kRun; ++u) av[j].v[u] *= bv.v[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      if (u < n) {
+        __builtin_amdgcn_s_waitcnt(kWaitVm0);
+        asm volatile("" ::: "memory");
+        i32x8 B[MT];
+        float sc[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          B[j] = frag(NT + j);
+          sc[j] = av[j].v[0];
+#pragma unroll
+          for (int v = 1; v < kRun; ++v) sc[j] = u + back == v ? av[j].v[v] : sc[j];
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const i32x8 A = frag(i);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            const f32x4 p = mfma_blk(A, B[j]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc[j], acc[i][j][r]);
+          }
+        }
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);  // the slot has been read
+        asm volatile("" ::: "memory");
+        if (u + 1 < n) issue(k0 + u + 1);
+      }
+    }
+  }
+
+  __syncthreads();  // the slots are no longer used
+  float(*part)[16 * MT][16 * NT] = reinterpret_cast<float(*)[16 * MT][16 * NT]>(smem);
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) *reinterpret_cast<f32x4*>(&part[wave][16 * j + c][16 * i + 4 * g]) = acc[i][j];
+  __syncthreads();
+  // four columns of a row per thread, the waves' sums in order
+  for (int q = tid; q < 16 * MT * 4 * NT; q += W * 64) {
+    const int row = q / (4 * NT), col = 4 * (q % (4 * NT)), m = t.t0 + row, n = n0 + col;
+    if (m >= t.end || n >= N) continue;
+    f32x4 y = *reinterpret_cast<const f32x4*>(&part[0][row][col]);
+#pragma unroll
+    for (int v = 1; v < W; ++v) y += *reinterpret_cast<const f32x4*>(&part[v][row][col]);
+    if (a.bias) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] += bf16_to_f32(a.bias[min(n + r, N - 1)]);
+    }
+    uint16_t* p = a.Y + (int64_t)m * N + n;
+    if ((N & 3) == 0) {
+      *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)f32_to_bf16(y[0]) | ((uint32_t)f32_to_bf16(y[1]) << 16),
+                                           (uint32_t)f32_to_bf16(y[2]) | ((uint32_t)f32_to_bf16(y[3]) << 16)};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < N) p[r] = f32_to_bf16(y[r]);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- LDS-tiled kernel
@@ -111,57 +270,65 @@ __global__ __launch_bounds__(256) void k_block_direct(BlockGemmArgs a) {
 // whole rows of 128 bytes per instruction, NS stages deep, chunks of a row
 // XOR-swizzled by the choice of the chunk each lane reads (blk_pos).
 //
-// The products sa * sb of the tile's scales wait in LDS too, four steps at a
-// time ([buffer][128-column block][row][4]): the BM first threads load four
-// scales of one activation row at once, which costs a quarter of the line
-// requests of one load per step.
+// With KS > 1, KS such groups of waves split K, each with its own stages, and add
+// up their sums in LDS at the end: tiles too few to fill the chip finish sooner.
 //
-// Step: a wave holds its TM activation fragments and streams its TN weight
-// fragments, read two fragments ahead; each meets TM MFMAs, and the VALU scales
-// and adds every result three MFMAs later.  All LDS reads of a stage are done two
-// fragments before the step's end; there the waves meet at the step's one
-// barrier, and the last two fragments' MFMAs cover the first reads of the next
-// stage.
-constexpr int kScaleSteps = 4;
+// The scales come the same way, 8 steps' at a time and two buffers deep: 8 rows
+// x 8 scales per instruction, in LDS row r's scale of step k at 8 r + (k + r / 8
+// % 2) % 8 (16 rows on distinct banks).  Through registers their wait drained
+// the loads under way every few steps (256 x 4096 x 4096: 13.9 us, 11.7 without
+// any scales).
+//
+// Step with two or three stages (larger tiles): a wave holds its TM activation
+// fragments and streams its TN weight fragments, read two ahead; each meets TM
+// MFMAs, and the VALU scales and adds every result three MFMAs later.  All LDS
+// reads of a stage are done two fragments before the step's end; there the waves
+// meet at the step's one barrier, and the last two fragments' MFMAs cover the
+// first reads of the next stage.
+// Step with four stages (smaller tiles, whose MFMAs are too few to cover reads
+// within the step): every fragment is read a whole step ahead into a second set
+// of registers; the waves meet at the step's start and refill the stage of the
+// step before.
+constexpr int kScaleSteps = 8;
 
-// LDS slot of 16-byte chunk k of row r: the four lane groups' reads of 16 rows
-// then fall on distinct banks.
-__device__ __forceinline__ int blk_pos(int r, int k) { return k ^ (((r >> 1) & 1) | (r & 4)); }
-
-template <int BN, int BM, int WN, int WM, int NS>
+template <int BN, int BM, int WN, int WM, int NS, int KS>
 struct TileT {
   static constexpr int WAVES = WN * WM, TN = BN / (16 * WN), TM = BM / (16 * WM);
   static constexpr int STAGE = (BN + BM) * 128;
   static constexpr int NB = BN / 128 ? BN / 128 : 1;  // 128-column blocks
-  static constexpr int SBUF = NB * BM * 4 * kScaleSteps;
+  static constexpr int SROWS = BM / (8 * WAVES);          // scale loads per wave
+  static constexpr int SBUF = BM * 4 * kScaleSteps + 256;  // scales of rows, then of columns
   static constexpr int PITCH = TN * 32 + 16;  // output tile row in LDS
-  static constexpr int OUT = WAVES * TM * 16 * PITCH;
-  static constexpr int MAIN = NS * STAGE + 2 * SBUF;
+  static constexpr int PART = BN * 4 + 16;    // row of fp32 sums in LDS (KS > 1)
+  static constexpr int OUT = KS > 1 ? KS * BM * PART : WAVES * TM * 16 * PITCH;
+  static constexpr int PARK = WAVES * 64 * 4 * SROWS;  // offsets of the scale loads
+  static constexpr int GROUP = NS * STAGE + 2 * SBUF + PARK;
+  static constexpr int MAIN = KS * GROUP;
   static constexpr int SMEM = MAIN > OUT ? MAIN : OUT;
-  static_assert(BM <= WAVES * 64, "a thread per row of scales");
   static_assert(BN % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole loads of 8 rows");
+  static_assert(WAVES % 2 == 0 && NB <= 8 && NS < kScaleSteps, "scale buffers");
 };
 
-template <int BN, int BM, int WN, int WM, int NS>
-__global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
-  using T = TileT<BN, BM, WN, WM, NS>;
+template <int BN, int BM, int WN, int WM, int NS, int KS>
+__global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
+  using T = TileT<BN, BM, WN, WM, NS, KS>;
   constexpr int TN = T::TN, TM = T::TM, W = T::WAVES;
   constexpr int LJW = BN / (8 * W), LJ = (BN + BM) / (8 * W);  // loads per wave and step: weights, all
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  float* sc = reinterpret_cast<float*>(smem + NS * T::STAGE);
-  const int tid = threadIdx.x, lane = tid & 63;
+  extern __shared__ __attribute__((aligned(16))) unsigned char shared[];
+  const int group = KS > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / (W * 64)) : 0;
+  const int tid = (int)threadIdx.x - group * W * 64, lane = tid & 63;  // within the group
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  unsigned char* smem = shared + group * T::GROUP;
+  unsigned char* sc = smem + NS * T::STAGE;
   const int g = lane >> 4, c = lane & 15;
   const int wn = wave % WN, wm = wave / WN;
   const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
 
-  // XCD-aware tile order: workgroup b runs on XCD b % 8; each XCD takes a
-  // contiguous piece of an order that fills bands of 4 column tiles row tile
-  // by row tile, so tiles in flight on one L2 share operands both ways
+  // bands of 4 column tiles, row tile by row tile: tiles in flight on one XCD
+  // share operands both ways
   int tx, ty;
   {
-    const int G = gx * gy, b = blockIdx.x, q = G >> 3, r = G & 7, x = b & 7;
-    const int idx = x * q + min(x, r) + (b >> 3);
+    const int idx = xcd_order(gx * gy);
     const int band = idx / (4 * gy), in = idx - band * 4 * gy, wide = min(4, gx - 4 * band);
     ty = in / wide;
     tx = 4 * band + in - ty * wide;
@@ -185,50 +352,49 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, 
     const int r = (j * W + wave) * 8 + lr;
     voff[j] = (uint32_t)(j < LJW ? min(r, N - n0 - 1) : min(r - BN, t.end - t.t0 - 1));
   }
-  const int srow = t.t0 + min(tid, t.end - t.t0 - 1);  // the row whose scales thread tid < BM stages
-  int ssrc = srow;
   uint32_t limit = 0xFFFFFFFFu;  // source rows from here on read as zeros
   if (a.rows) {
     limit = (uint32_t)a.M;
-    ssrc = a.rows[srow];
 #pragma unroll
     for (int j = LJW; j < LJ; ++j) voff[j] = (uint32_t)a.rows[t.t0 + voff[j]];
   }
+  // the loads of scales take the same rows as those of activations
+  const int KB4 = KB * 4, kpos = ((lane & 7) - (wave & 1)) & 7;
+  uint32_t* park = reinterpret_cast<uint32_t*>(sc + 2 * T::SBUF) + tid;  // kept in LDS: registers are short
+#pragma unroll
+  for (int j = 0; j < T::SROWS; ++j) park[j * W * 64] = voff[LJW + j] < limit ? voff[LJW + j] * (uint32_t)KB4 : kOut;
 #pragma unroll
   for (int j = 0; j < LJ; ++j)
     voff[j] = j < LJW || voff[j] < limit ? voff[j] * (uint32_t)K + kc16 : kOut;
+  // this group's steps: blocks k0 .. k0 + per - 1; from klimit on they read zeros
+  constexpr bool AHEAD = NS > 3;  // steps in pairs
+  const int per = (KB + KS - 1) / KS, steps = AHEAD ? (per + 1) & ~1 : per;
+  const int k0 = group * per, klimit = min(K, (k0 + per) * 128);
   auto issue1 = [&](int kt, int st, int j) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         j < LJW ? Wr : Xr, (__attribute__((address_space(3))) void*)(smem + st * T::STAGE + (j * W + wave) * 1024), 16,
-        (int)(kt * 128 + kc16 < K ? voff[j] : kOut), min(kt, KB - 1) * 128, 0, 0);
+        (int)(kt * 128 + kc16 < klimit ? voff[j] : kOut), min(kt, KB - 1) * 128, 0, 0);
   };
 
-  // scales of steps [first(ch), first(ch) + 4): thread `tid` owns row tid
-  const float* sa = nullptr;  // its activation row's scales (null: a row without any)
-  if (tid < BM && (uint32_t)ssrc < (uint32_t)a.M) sa = a.Xs + (int64_t)ssrc * KB;
-  const float* sb = a.Ws + ((int64_t)t.e * NBLK + n0 / 128) * KB;
-  auto first = [&](int ch) { return max(0, min(kScaleSteps * ch, KB - kScaleSteps)); };
-  typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-  auto load4 = [&](const float* p) {
-    if (KB >= kScaleSteps) return f32x4(*reinterpret_cast<const f32x4u*>(p));
-    return f32x4{p[0], p[min(1, KB - 1)], p[min(2, KB - 1)], p[KB - 1]};
-  };
-  f32x4 sav, sbv[T::NB];
-  auto load_scales = [&](int ch) {
-    sav = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (sa) {
-      sav = load4(sa + first(ch));
+  // scales of this group's steps 8 ch .. 8 ch + 7 (past the blocks the last one's), into buffer ch % 2
+  const __amdgpu_buffer_rsrc_t Sr =
+      a.rows ? make_rsrc(a.Xs, (uint32_t)((int64_t)a.M * KB4))
+             : make_rsrc(a.Xs + (int64_t)t.t0 * KB, (uint32_t)min(BM, t.end - t.t0) * (uint32_t)KB4);
+  const __amdgpu_buffer_rsrc_t Vr = make_rsrc(a.Ws + ((int64_t)t.e * NBLK + n0 / 128) * KB,
+                                              (uint32_t)min(T::NB, NBLK - n0 / 128) * (uint32_t)KB4);
+  auto fetch_scales = [&](int ch) {
+    unsigned char* to = sc + (ch & 1) * T::SBUF;
+    const int at = k0 + kScaleSteps * ch;
 #pragma unroll
-      for (int q = 0; q < T::NB; ++q) sbv[q] = load4(sb + (int64_t)min(q, NBLK - 1 - n0 / 128) * KB + first(ch));
+    for (int j = 0; j < T::SROWS; ++j) {
+      const uint32_t row = park[j * W * 64];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(Sr, (__attribute__((address_space(3))) void*)(to + (j * W + wave) * 256), 4,
+                                               (int)(row == kOut ? kOut : row + 4u * min(at + kpos, KB - 1)), 0, 0, 0);
     }
-  };
-  auto store_scales = [&](int ch) {
-    if (tid < BM) {
-#pragma unroll
-      for (int q = 0; q < T::NB; ++q)
-        *reinterpret_cast<f32x4*>(sc + ((ch & 1) * T::NB + q) * BM * kScaleSteps + tid * kScaleSteps) =
-            sa ? sav * sbv[q] : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    if (wave == 0)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          Vr, (__attribute__((address_space(3))) void*)(to + BM * 4 * kScaleSteps), 4,
+          (int)(lr < T::NB ? (uint32_t)(lr * KB4) + 4u * min(at + (lane & 7), KB - 1) : kOut), 0, 0, 0);
   };
 
   // operand fragments: rows 16 i + c of the wave's part, K 32 g .. 32 g + 31 = chunks 2g, 2g + 1
@@ -239,10 +405,23 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, 
     const unsigned char* p = base + st * T::STAGE + i * 2048;
     return join(*reinterpret_cast<const u32x4*>(p + flo), *reinterpret_cast<const u32x4*>(p + (flo ^ 16)));
   };
-  const float* scw = sc + ((wn * TN * 16) / 128 * BM + wm * TM * 16 + c) * kScaleSteps;
-  auto scale = [&](int kt, int i) {
-    const int ch = kt / kScaleSteps;
-    return scw[(ch & 1) * T::NB * BM * kScaleSteps + i * 16 * kScaleSteps + kt - first(ch)];
+  const unsigned char* sx = sc + (wm * TM * 16 + c) * 4 * kScaleSteps;
+  const unsigned char* sw = sc + BM * 4 * kScaleSteps + wn * TN * 16 / 128 * 4 * kScaleSteps;
+  // a step's scales: the lane's rows' and the column block's, multiplied once they have landed (a step past the
+  // blocks multiplies zeros)
+  struct StepScales {
+    float s[TM], w;
+  };
+  auto read_scales = [&](int n, StepScales& v) {
+    const int buf = (n / kScaleSteps & 1) * T::SBUF, k = n % kScaleSteps;
+    v.w = *reinterpret_cast<const float*>(sw + buf + 4 * k);
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+      v.s[j] = *reinterpret_cast<const float*>(sx + buf + j * 64 * kScaleSteps + 4 * ((k + (c >> 3)) & 7));
+  };
+  auto join_scales = [&](int n, StepScales& v) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) v.s[j] = (KS == 1 && !AHEAD) || (n < per && k0 + n < KB) ? v.s[j] * v.w : 0.f;
   };
 
   f32x4 acc[TN][TM];
@@ -251,154 +430,284 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, 
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  load_scales(0);
+  fetch_scales(0);
 #pragma unroll
   for (int st = 0; st < NS - 1; ++st)
 #pragma unroll
-    for (int j = 0; j < LJ; ++j) issue1(st, st, j);
-  store_scales(0);
-  __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
-  asm volatile("s_barrier" ::: "memory");
-  // A freed stage's loads are spread over SPAN fragments' MFMAs (two of the
-  // step that frees it, the rest of the next one): issued in one go they fill
-  // the memory pipe's queue and the waves stall on it.
-  constexpr int SPAN = TN >= 8 ? TN - 2 : TN - 1;
-  auto slot = [](int l) { return l * SPAN / LJ; };
-#pragma unroll
-  for (int l = 0; l < LJ; ++l)
-    if (slot(l) < 2) issue1(NS - 1, NS - 1, l);
+    for (int j = 0; j < LJ; ++j) issue1(k0 + st, st, j);
 
-  // ring of weight fragments: fragment i in slot i % R, so that the next step's
-  // first two find slots 0 and 1 free at the end of this step
-  constexpr int R = TN % 3 == 2 ? 3 : 4;
-  static_assert(TN % R == 2 || TN % R == 0, "slots 0 and 1 are free in time");
-  i32x8 A[R], B[TM];
   // products, scaled and added LAG MFMAs after they were made: fewer, and the VALU would wait for their results
-  constexpr int LAG = 3;
+  constexpr int LAG = 3, Q = TN * TM;
   f32x4 p[LAG + 1];
-  float s[TM];
-  A[0] = frag(fw, 0, 0);
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    B[j] = frag(fx, 0, j);
-    s[j] = scale(0, j);
-  }
-  A[1] = frag(fw, 0, 1);
-  auto add = [&](int q) {
+  auto add = [&](int q, const StepScales& v) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      acc[q / TM][q % TM][r] = __builtin_fmaf(p[q % (LAG + 1)][r], s[q % TM], acc[q / TM][q % TM][r]);
+      acc[q / TM][q % TM][r] = __builtin_fmaf(p[q % (LAG + 1)][r], v.s[q % TM], acc[q / TM][q % TM][r]);
   };
-  // one step; `pst`, `st`, `nst`: the stages of the last, this and the next one
-  auto step = [&](int kt, int pst, int st, int nst) {
-    constexpr int Q = TN * TM, MEET = (TN - 2) * TM;
+  auto settle = [&] {
+    // the sums are due here: the compiler would sink the scaling past the branch between the steps and keep the
+    // step's products in registers
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q / TM, j = q % TM;
-      if (j == 0 && i + 2 < TN) A[(i + 2) % R] = frag(fw, st, i + 2);
-      if (q == MEET) {
-        // every read of this stage has been made: meet, then refill it
-        __builtin_amdgcn_s_waitcnt((kWaitVm0 & kWaitLgkm0) | ((NS - 2) * LJ & 15) | (((NS - 2) * LJ >> 4) << 14));
-        asm volatile("s_barrier" ::: "memory");
-        const int sub = kt & (kScaleSteps - 1);
-        if (sub == 0) load_scales(kt / kScaleSteps + 1);
-        if (sub == 2) store_scales(kt / kScaleSteps + 1);
-      }
-      p[q % (LAG + 1)] = mfma_blk(A[i % R], B[j]);
-      if (q >= LAG) add(q - LAG);
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int l = 0; l < LJ; ++l) {
-        // in a slot's first MFMAs, one load each
-        const int at = slot(l), nth = l - (at * LJ + SPAN - 1) / SPAN;
-        if (j == min(nth, TM - 1)) {
-          if (at < 2 && i == TN - 2 + at) issue1(kt + NS, st, l);
-          if (at >= 2 && i == at - 2) issue1(kt + NS - 1, pst, l);
-        }
-      }
-      if (q == MEET + TM - 1) A[0] = frag(fw, nst, 0);
-      if (i == TN - 1) B[j] = frag(fx, nst, j);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int q = Q - LAG; q < Q; ++q) add(q);
-    A[1] = frag(fw, nst, 1);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) s[j] = scale(min(kt + 1, KB - 1), j);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < TM; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
-  for (int kt = 0, pst = NS - 1, st = 0; kt < KB; ++kt) {
-    const int nst = st + 1 == NS ? 0 : st + 1;
-    step(kt, pst, st, nst);
-    pst = st;
-    st = nst;
-  }
+  // this wave's loads but for the newest N have landed, and its LDS reads; meet the others
+#define WQ_MEET(N)                                                                                        \
+  do {                                                                                                    \
+    __builtin_amdgcn_s_waitcnt((kWaitVm0 & kWaitLgkm0) | ((N) & 15) | (((N) >> 4) << 14));                \
+    asm volatile("s_barrier" ::: "memory");                                                               \
+  } while (0)
 
-  // output: wave tiles leave through LDS as 16-byte row pieces
-  __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
-  asm volatile("s_barrier" ::: "memory");
-  unsigned char* et = smem + wave * (TM * 16 * T::PITCH);
-  const int nw = n0 + wn * TN * 16, mw = t.t0 + wm * TM * 16;
+  if constexpr (AHEAD) {
+    WQ_MEET((NS - 2) * LJ);
+    struct Operands {
+      i32x8 a[TN], b[TM];
+      StepScales s;
+    } set[2];
 #pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias) {
+    for (int i = 0; i < TN; ++i) set[0].a[i] = frag(fw, 0, i);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) b[r] = bf16_to_f32(a.bias[min(nw + 16 * i + 4 * g + r, N - 1)]);
+    for (int j = 0; j < TM; ++j) set[0].b[j] = frag(fx, 0, j);
+    read_scales(0, set[0].s);
+    // step n on `now`, reading step n + 1's operands into `next`; `pst`, `nst`: the stages of the step before and of
+    // the next one
+    auto step = [&](int n, int pst, int nst, Operands& now, Operands& next) {
+      WQ_MEET((NS - 3) * LJ);
+      join_scales(n, now.s);
+      read_scales(n + 1, next.s);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        constexpr int F = TN + TM;
+#pragma unroll
+        for (int f = 0; f < F; ++f)  // next operands in the order of their use, spread over the step
+          if (q == f * Q / F) {
+            if (f == 0) next.a[0] = frag(fw, nst, 0);
+            else if (f <= TM) next.b[f - 1] = frag(fx, nst, f - 1);
+            else next.a[f - TM] = frag(fw, nst, f - TM);
+          }
+        p[q % (LAG + 1)] = mfma_blk(now.a[q / TM], now.b[q % TM]);
+        if (q >= LAG) add(q - LAG, now.s);
+#pragma unroll
+        for (int l = 0; l < LJ; ++l)
+          if (q == l * Q / LJ) issue1(k0 + n - 1 + NS, pst, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = Q - LAG; q < Q; ++q) add(q, now.s);
+      settle();
+    };
+    auto after = [](int st) { return st + 1 == NS ? 0 : st + 1; };
+    for (int n = 0, pst = NS - 1, st = 0; n < steps; n += 2) {
+      const int st1 = after(st), st2 = after(st1);
+      step(n, pst, st1, set[0], set[1]);
+      step(n + 1, st, st2, set[1], set[0]);
+      if (n % kScaleSteps == 0) fetch_scales(n / kScaleSteps + 1);
+      pst = st1;
+      st = st2;
     }
+  } else {
+    WQ_MEET(0);
+    // A freed stage's loads are spread over SPAN fragments' MFMAs (two of the
+    // step that frees it, the rest of the next one): issued in one go they fill
+    // the memory pipe's queue and the waves stall on it.
+    constexpr int SPAN = TN >= 8 ? TN - 2 : TN - 1;
+    auto slot = [](int l) { return l * SPAN / LJ; };
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      u32x2 v;
+    for (int l = 0; l < LJ; ++l)
+      if (slot(l) < 2) issue1(k0 + NS - 1, NS - 1, l);
+
+    // ring of weight fragments: fragment i in slot i % R, so that the next step's
+    // first two find slots 0 and 1 free at the end of this step
+    constexpr int R = TN % 3 == 2 ? 3 : 4;
+    static_assert(TN % R == 2 || TN % R == 0, "slots 0 and 1 are free in time");
+    i32x8 A[R], B[TM];
+    StepScales S;
+    A[0] = frag(fw, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[h] = (uint32_t)f32_to_bf16(acc[i][j][2 * h] + b[2 * h]) |
-               ((uint32_t)f32_to_bf16(acc[i][j][2 * h + 1] + b[2 * h + 1]) << 16);
-      *reinterpret_cast<u32x2*>(et + (16 * j + c) * T::PITCH + (16 * i + 4 * g) * 2) = v;
+    for (int j = 0; j < TM; ++j) B[j] = frag(fx, 0, j);
+    read_scales(0, S);
+    A[1] = frag(fw, 0, 1);
+    // step n; `pst`, `st`, `nst`: the stages of the last, this and the next one
+    auto step = [&](int n, int pst, int st, int nst) {
+      const int kt = k0 + n;
+      constexpr int MEET = (TN - 2) * TM;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int i = q / TM, j = q % TM;
+        if (j == 0 && i + 2 < TN) A[(i + 2) % R] = frag(fw, st, i + 2);
+        if (q == MEET) WQ_MEET((NS - 2) * LJ);  // every read of this stage has been made: meet, then refill it
+        p[q % (LAG + 1)] = mfma_blk(A[i % R], B[j]);
+        if (q == LAG - 1) join_scales(n, S);
+        if (q >= LAG) add(q - LAG, S);
+#pragma unroll
+        for (int l = 0; l < LJ; ++l) {
+          // in a slot's first MFMAs, one load each
+          const int at = slot(l), nth = l - (at * LJ + SPAN - 1) / SPAN;
+          if (j == min(nth, TM - 1)) {
+            if (at < 2 && i == TN - 2 + at) issue1(kt + NS, st, l);
+            if (at >= 2 && i == at - 2) issue1(kt + NS - 1, pst, l);
+          }
+        }
+        if (q == MEET + TM - 1) A[0] = frag(fw, nst, 0);
+        if (i == TN - 1) B[j] = frag(fx, nst, j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = Q - LAG; q < Q; ++q) add(q, S);
+      settle();
+      A[1] = frag(fw, nst, 1);
+      read_scales(n + 1, S);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int n = 0, pst = NS - 1, st = 0; n < steps; ++n) {
+      const int nst = st + 1 == NS ? 0 : st + 1;
+      step(n, pst, st, nst);
+      if (n % kScaleSteps == 0) fetch_scales(n / kScaleSteps + 1);
+      pst = st;
+      st = nst;
     }
   }
-  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  asm volatile("" ::: "memory");
-  constexpr int LPR = TN * 2, RPI = 64 / LPR;  // lanes per row, rows per store instruction
+#undef WQ_MEET
+
+  __builtin_amdgcn_s_waitcnt(kWaitVm0 & kWaitLgkm0);
+  asm volatile("s_barrier" ::: "memory");  // the stages are no longer used
   const bool vec = (N & 7) == 0;
+  auto put = [&](int m, int n, u32x4 v) {  // 8 columns of a row
+    if (m >= t.end) return;
+    uint16_t* y = a.Y + (int64_t)m * N + n;
+    if (vec) {
+      if (n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
+    } else {
 #pragma unroll
-  for (int q = 0; q < TM * 16 / RPI; ++q) {
-    const int row = RPI * q + lane / LPR, col = 8 * (lane % LPR);
-    const u32x4 v = *reinterpret_cast<const u32x4*>(et + row * T::PITCH + col * 2);
-    const int m = mw + row, n = nw + col;
-    if (m < t.end) {
-      uint16_t* y = a.Y + (int64_t)m * N + n;
-      if (vec) {
-        if (n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
-      } else {
+      for (int e = 0; e < 8; ++e)
+        if (n + e < N) y[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+  };
+  auto bias = [&](int n) { return a.bias ? bf16_to_f32(a.bias[min(n, N - 1)]) : 0.f; };
+  auto pack = [](float lo, float hi) { return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16); };
+
+  if constexpr (KS > 1) {
+    // the groups' sums meet in LDS and are added in order, 8 columns of a row per thread
+    const int col = wn * TN * 16 + 4 * g, row = wm * TM * 16 + c;
+    unsigned char* mine = shared + group * (BM * T::PART);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < N) y[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-      }
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        *reinterpret_cast<f32x4*>(mine + (row + 16 * j) * T::PART + (col + 16 * i) * 4) = acc[i][j];
+    __syncthreads();
+    for (int q = threadIdx.x; q < BM * BN / 8; q += KS * W * 64) {
+      const int r = q / (BN / 8), n = 8 * (q % (BN / 8));
+      f32x4 y[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          y[h] += *reinterpret_cast<const f32x4*>(shared + (k * BM + r) * T::PART + n * 4 + 16 * h);
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = pack(y[e >> 1][2 * (e & 1)] + bias(n0 + n + 2 * e), y[e >> 1][2 * (e & 1) + 1] + bias(n0 + n + 2 * e + 1));
+      put(t.t0 + r, n0 + n, v);
+    }
+  } else {
+    // wave tiles leave through LDS as 16-byte row pieces
+    unsigned char* et = shared + wave * (TM * 16 * T::PITCH);
+    const int nw = n0 + wn * TN * 16, mw = t.t0 + wm * TM * 16;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      float b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = bias(nw + 16 * i + 4 * g + r);
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        *reinterpret_cast<u32x2*>(et + (16 * j + c) * T::PITCH + (16 * i + 4 * g) * 2) =
+            u32x2{pack(acc[i][j][0] + b[0], acc[i][j][1] + b[1]), pack(acc[i][j][2] + b[2], acc[i][j][3] + b[3])};
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    asm volatile("" ::: "memory");
+    constexpr int LPR = TN * 2, RPI = 64 / LPR;  // lanes per row, rows per store instruction
+#pragma unroll
+    for (int q = 0; q < TM * 16 / RPI; ++q) {
+      const int row = RPI * q + lane / LPR, col = 8 * (lane % LPR);
+      put(mw + row, nw + col, *reinterpret_cast<const u32x4*>(et + row * T::PITCH + col * 2));
     }
   }
 }
 
 }  // namespace
 
-template <int BN, int BM, int WN, int WM, int NS>
+// Row tiles of bm rows; for experts a bound on their number: every expert that has rows may end in a partial tile.
+static int64_t row_tiles(const BlockGemmArgs& a, int64_t bm) {
+  if (!a.offsets) return (a.M + bm - 1) / bm;
+  return (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * (bm - 1)) / bm;
+}
+
+template <int BN, int BM, int WN, int WM, int NS, int KS>
 static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
-  using T = TileT<BN, BM, WN, WM, NS>;
+  using T = TileT<BN, BM, WN, WM, NS, KS>;
+  static_assert(T::SMEM <= 160 * 1024, "LDS of a CU");
   static std::atomic<int> allowed{0};
-  const auto kern = k_block_tile<BN, BM, WN, WM, NS>;
+  const auto kern = k_block_tile<BN, BM, WN, WM, NS, KS>;
   hipError_t e = allow_smem(kern, T::SMEM, allowed);
   if (e != hipSuccess) return e;
-  const int64_t gx = (a.N + BN - 1) / BN;
-  const int64_t gy = a.offsets ? (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
-  kern<<<(unsigned)(gx * gy), WN * WM * 64, T::SMEM, s>>>(a, (int)gx, (int)gy);
+  const int64_t gx = (a.N + BN - 1) / BN, gy = row_tiles(a, BM);
+  kern<<<(unsigned)(gx * gy), KS * WN * WM * 64, T::SMEM, s>>>(a, (int)gx, (int)gy);
   return hipGetLastError();
 }
 
-hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
-  if (a.T >= 1024) return tile_launch<256, 256, 2, 4, 2>(a, s);
-  if (a.T >= 128) return tile_launch<128, 128, 2, 2, 2>(a, s);
-  // row tiles of 16: every expert with rows may end in a partial one
-  const int64_t tiles = a.offsets ? (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * 15) / 16 : (a.M + 15) / 16;
-  k_block_direct<<<dim3((unsigned)((a.N + 63) / 64), (unsigned)tiles), 256, 0, s>>>(a);
+template <int NT, int MT, int W>
+static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
+  constexpr int smem = StreamT<NT, MT, W>::SMEM;
+  static_assert(smem <= 65536, "no leave needed for the LDS size");
+  const int64_t gx = (a.N + 16 * NT - 1) / (16 * NT), gy = row_tiles(a, 16 * MT);
+  k_block_stream<NT, MT, W><<<(unsigned)(gx * gy), W * 64, smem, s>>>(a, (int)gx, (int)gy);
   return hipGetLastError();
+}
+
+// Which form.  Times in us, of graphs of back-to-back launches.
+hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
+  if (a.offsets) {
+    // By an expert's rows on average.  Few: the weights are streamed, 64 columns to a workgroup, so that fewer of
+    // them look for their rows (64 rows of 32 experts, 2048 x 2048: 17 against 24 with 16 columns and 22 with
+    // 256 x 128 tiles; 16 rows each: 26 against 39).  More: wide tiles, again to have few workgroups (31 rows each,
+    // 64 experts 1536 x 2048: 46 against 52 streamed; 62 rows each, 2048 x 2048: 41 against 44 with 64 x 64 tiles
+    // and 54 streamed); 256 rows to a tile from 512 on (172 against 173 at 1024, less traffic).
+    const int rows = (a.T + a.E - 1) / a.E;
+    if (rows <= 16) return stream_launch<4, 1, 4>(a, s);
+    if (rows < 512) return tile_launch<256, 128, 4, 2, 3, 1>(a, s);
+    return tile_launch<256, 256, 2, 4, 2, 1>(a, s);
+  }
+  if (a.M <= 64) {
+    // Streamed.  Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best with
+    // the smallest workgroups' tiles (1 x 4096 x 3072: 4.7 against 5.9 with 32 columns), many share what they read
+    // (32 x 8192 x 8192: 13.1 against 16.2 with 16 columns; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
+    const int64_t tiles = ((a.N + 15) / 16) * (int64_t)((a.M + 15) / 16);
+    if (tiles <= 512) return stream_launch<1, 1, 8>(a, s);
+    if (tiles <= 1024 || a.M <= 16) return stream_launch<2, 1, 4>(a, s);
+    return stream_launch<2, 2, 4>(a, s);
+  }
+  // Tiles: the form with the least time for its rounds of 256 workgroups, from each form's time for one scale
+  // block of K (measured at N = K = 4096, 32 blocks, one full round of tiles: 65, 37, 24, 15 and 11 us in all).
+  struct Form {
+    int bn, bm;
+    float per_block;  // us
+    hipError_t (*launch)(const BlockGemmArgs&, hipStream_t);
+  };
+  static const Form forms[] = {{256, 256, 1.95f, tile_launch<256, 256, 2, 4, 2, 1>},
+                               {256, 128, 1.05f, tile_launch<256, 128, 4, 2, 3, 1>},
+                               {128, 128, 0.62f, tile_launch<128, 128, 2, 4, 4, 1>},
+                               {128, 64, 0.34f, tile_launch<128, 64, 2, 2, 3, 2>},
+                               {64, 64, 0.24f, tile_launch<64, 64, 2, 2, 4, 2>}};
+  const Form* best = nullptr;
+  float least = 0.f;
+  for (const Form& f : forms) {
+    const int64_t tiles = ((a.N + f.bn - 1) / f.bn) * (int64_t)((a.M + f.bm - 1) / f.bm);
+    const float t = (float)((tiles + 255) / 256) * f.per_block;
+    if (!best || t < least) best = &f, least = t;
+  }
+  return best->launch(a, s);
 }
 
 }  // namespace wq
