@@ -10,10 +10,10 @@
  *                        (a plain Linear is E = 1)
  * The quantizer, for every block of fp32 values y:
  *   s    = max(amax / 448, 2^-126), amax = max |y|, one IEEE fp32 division
- *   code = E4M3(clamp(y / s, +-448)), nearest even, the sign of zero kept; the
- *          quotient is evaluated as y * (1 / s) in fp32 (1 / s correctly rounded),
- *          at most 1.5 fp32 ulp from y / s.  The floor 2^-126 keeps 1 / s finite:
- *          an all-zero block has that scale and codes 0.
+ *   code = E4M3(y / s), nearest even, the sign of zero kept; the fp32 quotient is
+ *          within one ulp of IEEE division's, and by the choice of s at most 448.
+ *          The floor 2^-126 keeps 1 / s finite: an all-zero block has that scale
+ *          and codes 0.
  * A block that holds a NaN has the scale NaN, one that holds an infinity (and no
  * NaN) the scale infinity: no finite value is made up for it.
  *
@@ -72,7 +72,8 @@ wq_status wq_block_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* 
  * Gated activation with a quantized result: GU holds rows of 2 K bf16 values
  * (row m at GU + m * ldg elements; ldg >= 2 K, ldg % 8 == 0), gate first;
  *   y[k] = silu(GU[m][k]) * GU[m][K + k],  silu(g) = g / (1 + exp(-g))
- * in fp32.  Xq/Xs receive y quantized.
+ * in fp32 (-0 for g < -88.6, where exp(-g) leaves fp32's range).  Xq/Xs receive
+ * y quantized.
  */
 wq_status wq_block_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int64_t K, void* Xq, float* Xs,
                                      void* stream);

@@ -32,8 +32,7 @@ def quantize_rows(y):
     for b in range(blocks(K)):
         part = y[:, BLOCK * b : BLOCK * (b + 1)]
         scales[:, b] = _scale(np.abs(part).max(axis=1))
-        inv = np.float32(1) / scales[:, b]
-        v = (part * inv[:, None]).astype(np.float32)
+        v = (part / scales[:, b, None]).astype(np.float32)
         codes[:, BLOCK * b : BLOCK * (b + 1)] = e4m3_encode(np.clip(v, np.float32(-448), np.float32(448)))
     return codes, scales
 
@@ -47,8 +46,7 @@ def quantize_weight(W_bits):
         for b in range(blocks(K)):
             at = np.s_[BLOCK * i : BLOCK * (i + 1), BLOCK * b : BLOCK * (b + 1)]
             scales[i, b] = _scale(np.abs(w[at]).max())
-            inv = np.float32(1) / scales[i, b]
-            v = (w[at] * inv).astype(np.float32)
+            v = (w[at] / scales[i, b]).astype(np.float32)
             codes[at] = e4m3_encode(np.clip(v, np.float32(-448), np.float32(448)))
     return codes, scales
 

@@ -59,23 +59,58 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
   return s < kTiny ? kTiny : s;  // a NaN stays
 }
 
-__device__ __forceinline__ u32x2 codes8(const F8& y, float inv) {
+// E4M3 codes of y / s, the quotient as y * (1 / s) and one correction by its
+// remainder: IEEE division's result but for rare last bits, at a third of its
+// instructions.  (y * (1 / s) alone rounds four times as many codes to the
+// other neighbour as the fp32 definition does.)  |y / s| <= 448 by the choice
+// of s, so nothing is clamped.
+__device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
+  const float inv = 1.0f / s;
   F8 q;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q.v[i] = clampf(y.v[i] * inv, -448.f, 448.f);
+  for (int i = 0; i < 8; ++i) {
+    const float v = y.v[i] * inv;
+    q.v[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-v, s, y.v[i]), inv, v), v);  // (-0 would become 0)
+  }
   return u32x2{e4m3_pack4(q.v[0], q.v[1], q.v[2], q.v[3]), e4m3_pack4(q.v[4], q.v[5], q.v[6], q.v[7])};
+}
+
+// silu(g) u = g / (1 + exp(-g)) u within a few fp32 ulp.
+//   exp(-g) = 2^t, t = -g log2 e in two parts: the high part's power comes from
+//   the hardware's 2^x, the low part enters as 1 + low ln 2;
+//   the quotient is g' r with one correction by its remainder, r the hardware's
+//   reciprocal of d' (1 ulp).  d' = 2^-8 (1 + exp(-g)) and g' = 2^-8 g: r stays a
+//   normal number up to the largest d (reciprocals below 2^-126 read as 0).
+// Below -88.6 exp(-g) leaves fp32 and the result is -0 (its size is below
+// 3e-37); above 90 exp(-g) no longer counts.  A NaN stays one.
+// Two library calls (expf and division) took 45 instructions an element, more
+// than the memory's time (8192 x 8192: 75 us; its 335 MB at 5.7 TB/s: 59 us).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  constexpr float L = -1.4426950216293335f, Ll = -1.9259629911e-8f, ln2 = 0.69314718056f;  // -log2 e = L + Ll
+  constexpr float far = -88.6f;
+  const float x = __builtin_amdgcn_fmed3f(g, far, 90.0f);
+  const float hi = x * L;
+  const float lo = __builtin_fmaf(x, Ll, __builtin_fmaf(x, L, -hi));
+  float e = __builtin_amdgcn_exp2f(hi);
+  e = __builtin_fmaf(e, lo * ln2, e);
+  const float d = __builtin_fmaf(e, 0.00390625f, 0.00390625f), n = g * 0.00390625f;
+  const float r = __builtin_amdgcn_rcpf(d);
+  const float q = n * r;
+  return (g < far ? -0.0f : __builtin_fmaf(__builtin_fmaf(-q, d, n), r, q)) * u;
 }
 
 // ---------------------------------------------------------------- activation rows, gated activation
 // One lane per 8 elements, one 16-lane row per scale block; the blocks of all
 // rows are numbered through, so short rows share a workgroup.
+// The row of a block is blk / KB as a product: with 2^sh < KB <= 2^(sh + 1) and
+// magic = ceil(2^(32 + sh) / KB), exact for blk < 2^31 (KB = 1: magic = 0).
 template <bool GATE>
 __global__ __launch_bounds__(256) void k_block_quant_rows(const uint16_t* __restrict__ X, int64_t ldx, uint32_t nblk,
-                                                          uint32_t KB, uint32_t K, uint8_t* __restrict__ Xq,
-                                                          float* __restrict__ Xs) {
+                                                          uint32_t KB, uint32_t magic, uint32_t sh, uint32_t K,
+                                                          uint8_t* __restrict__ Xq, float* __restrict__ Xs) {
   const uint32_t blk = blockIdx.x * 16u + (threadIdx.x >> 4);
   if (blk >= nblk) return;  // whole 16-lane rows leave together
-  const uint32_t m = blk / KB, k = (blk - m * KB) * 128u + (threadIdx.x & 15u) * 8u;
+  const uint32_t m = magic ? __umulhi(blk, magic) >> sh : blk, k = (blk - m * KB) * 128u + (threadIdx.x & 15u) * 8u;
   const bool in = k < K;  // K % 16 == 0: a lane's 8 elements are inside or outside together
   F8 y{};
   if (in) {
@@ -84,14 +119,14 @@ __global__ __launch_bounds__(256) void k_block_quant_rows(const uint16_t* __rest
     if constexpr (GATE) {
       const F8 u = unpack8(*reinterpret_cast<const u32x4*>(p + K));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y.v[i] = x.v[i] / (1.0f + expf(-x.v[i])) * u.v[i];
+      for (int i = 0; i < 8; ++i) y.v[i] = silu_mul(x.v[i], u.v[i]);
     } else {
       y = x;
     }
   }
   const float s = block_scale(max_row16(absmax8(y)));
   if (in) {
-    *reinterpret_cast<u32x2*>(Xq + (int64_t)m * K + k) = codes8(y, 1.0f / s);
+    *reinterpret_cast<u32x2*>(Xq + (int64_t)m * K + k) = codes8(y, s);
     if ((threadIdx.x & 15u) == 0) Xs[blk] = s;
   }
 }
@@ -164,7 +199,7 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void k_block_norm(BlockN
     if (in) {
       if (a.residual_out) *reinterpret_cast<u32x4*>(a.residual_out + m * K + c * 8u) = pack8(h[j]);
       if (a.y_out) *reinterpret_cast<u32x4*>(a.y_out + m * K + c * 8u) = pack8(y);
-      *reinterpret_cast<u32x2*>(a.Xq + m * K + c * 8u) = codes8(y, 1.0f / s);
+      *reinterpret_cast<u32x2*>(a.Xq + m * K + c * 8u) = codes8(y, s);
       if ((lane & 15) == 0) a.Xs[m * KB + c / 16u] = s;
     }
   }
@@ -193,11 +228,10 @@ __global__ __launch_bounds__(256) void k_block_quant_weight(const uint16_t* __re
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = amax;
   __syncthreads();
   const float s = block_scale(max(max(part[0], part[1]), max(part[2], part[3])));
-  const float inv = 1.0f / s;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int n = nb * 128 + 16 * j + (int)(threadIdx.x >> 4);
-    if (n < N && k < K) *reinterpret_cast<u32x2*>(codes + base + (int64_t)n * K + k) = codes8(y[j], inv);
+    if (n < N && k < K) *reinterpret_cast<u32x2*>(codes + base + (int64_t)n * K + k) = codes8(y[j], s);
   }
   if (threadIdx.x == 0) scales[((int64_t)blockIdx.z * NB + nb) * KB + kb] = s;
 }
@@ -208,10 +242,15 @@ hipError_t launch_block_quant_rows(bool gate, const uint16_t* X, int64_t ldx, in
                                    float* Xs, hipStream_t s) {
   const uint32_t KB = (uint32_t)((K + 127) / 128), nblk = (uint32_t)M * KB;
   const unsigned grid = (nblk + 15u) / 16u;
+  uint32_t sh = 0, magic = 0;
+  if (KB > 1) {
+    while ((2u << sh) < KB) ++sh;
+    magic = (uint32_t)((((uint64_t)1 << (32 + sh)) + KB - 1) / KB);
+  }
   if (gate)
-    k_block_quant_rows<true><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, (uint32_t)K, Xq, Xs);
+    k_block_quant_rows<true><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, magic, sh, (uint32_t)K, Xq, Xs);
   else
-    k_block_quant_rows<false><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, (uint32_t)K, Xq, Xs);
+    k_block_quant_rows<false><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, magic, sh, (uint32_t)K, Xq, Xs);
   return hipGetLastError();
 }
 
