@@ -309,7 +309,9 @@ struct TileT {
   static_assert(WAVES % 2 == 0 && NB <= 8 && NS < kScaleSteps, "scale buffers");
 };
 
-template <int BN, int BM, int WN, int WM, int NS, int KS>
+// TAIL: K % 128 != 0, chunks past K read zeros.  (Without it the loads carry no
+// mask; those of steps past the end read the last block again, unused.)
+template <int BN, int BM, int WN, int WM, int NS, int KS, bool TAIL>
 __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
   using T = TileT<BN, BM, WN, WM, NS, KS>;
   constexpr int TN = T::TN, TM = T::TM, W = T::WAVES;
@@ -366,14 +368,14 @@ __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs
 #pragma unroll
   for (int j = 0; j < LJ; ++j)
     voff[j] = j < LJW || voff[j] < limit ? voff[j] * (uint32_t)K + kc16 : kOut;
-  // this group's steps: blocks k0 .. k0 + per - 1; from klimit on they read zeros
+  // this group's steps: blocks k0 .. k0 + per - 1 (steps past those count nothing: their scales are zero)
   constexpr bool AHEAD = NS > 3;  // steps in pairs
   const int per = (KB + KS - 1) / KS, steps = AHEAD ? (per + 1) & ~1 : per;
-  const int k0 = group * per, klimit = min(K, (k0 + per) * 128);
+  const int k0 = group * per;
   auto issue1 = [&](int kt, int st, int j) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         j < LJW ? Wr : Xr, (__attribute__((address_space(3))) void*)(smem + st * T::STAGE + (j * W + wave) * 1024), 16,
-        (int)(kt * 128 + kc16 < klimit ? voff[j] : kOut), min(kt, KB - 1) * 128, 0, 0);
+        (int)(!TAIL || kt * 128 + kc16 < K ? voff[j] : kOut), min(kt, KB - 1) * 128, 0, 0);
   };
 
   // scales of this group's steps 8 ch .. 8 ch + 7 (past the blocks the last one's), into buffer ch % 2
@@ -511,7 +513,7 @@ __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs
     // A freed stage's loads are spread over SPAN fragments' MFMAs (two of the
     // step that frees it, the rest of the next one): issued in one go they fill
     // the memory pipe's queue and the waves stall on it.
-    constexpr int SPAN = TN >= 8 ? TN - 2 : TN - 1;
+    constexpr int SPAN = TN >= 8 ? 4 : TN - 1;
     auto slot = [](int l) { return l * SPAN / LJ; };
 #pragma unroll
     for (int l = 0; l < LJ; ++l)
@@ -648,9 +650,10 @@ template <int BN, int BM, int WN, int WM, int NS, int KS>
 static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   using T = TileT<BN, BM, WN, WM, NS, KS>;
   static_assert(T::SMEM <= 160 * 1024, "LDS of a CU");
-  static std::atomic<int> allowed{0};
-  const auto kern = k_block_tile<BN, BM, WN, WM, NS, KS>;
-  hipError_t e = allow_smem(kern, T::SMEM, allowed);
+  static std::atomic<int> allowed[2];
+  const bool tail = a.K % 128 != 0;
+  const auto kern = tail ? k_block_tile<BN, BM, WN, WM, NS, KS, true> : k_block_tile<BN, BM, WN, WM, NS, KS, false>;
+  hipError_t e = allow_smem(kern, T::SMEM, allowed[tail]);
   if (e != hipSuccess) return e;
   const int64_t gx = (a.N + BN - 1) / BN, gy = row_tiles(a, BM);
   kern<<<(unsigned)(gx * gy), KS * WN * WM * 64, T::SMEM, s>>>(a, (int)gx, (int)gy);
