@@ -22,7 +22,9 @@
  * nor allocate, every check on the host before anything is enqueued,
  * wq_last_error() for the reason.  Base pointers of codes and bf16 tensors
  * must be 16-byte aligned (a bias 2-byte), the other pointers aligned to their type.
- * K % 16 == 0 everywhere (WQ_ESHAPE otherwise).
+ * K % 16 == 0 everywhere (WQ_ESHAPE otherwise).  The row operators take fewer
+ * than 2^27 scale blocks a call, the products fewer tiles than a launch holds
+ * (some 2^23; WQ_EUNSUPPORTED otherwise).
  */
 #ifndef WQ_BLOCK_H
 #define WQ_BLOCK_H
@@ -91,7 +93,7 @@ wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K,
 /*
  * The same product for E experts over rows sorted by expert:
  *   Y[t] = X[rows[t]] . W[e]^T   for offsets[e] <= t < offsets[e + 1]
- *   Xq, Xs  : M rows of codes and scales
+ *   Xq, Xs  : M rows of codes and scales, M >= 1 where T >= 1
  *   rows    : int32 [T] on the device, each in [0, M) (a row of another value
  *             is read as zeros), or NULL: sorted row t reads X[t], and M == T
  *   offsets : int32 [E + 1] on the device, nondecreasing from offsets[0] = 0;

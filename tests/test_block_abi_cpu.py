@@ -73,6 +73,8 @@ def test_row_operators(call):
 def test_too_many_blocks():
     assert act(M=1 << 30, K=256, ldx=256) == wq.EUNSUPPORTED
     assert gate(M=1 << 30, K=256, ldx=512) == wq.EUNSUPPORTED
+    assert act(M=1 << 27, K=128, ldx=128) == wq.EUNSUPPORTED
+    assert norm(M=1 << 26, K=128, ldx=128) == wq.EUNSUPPORTED
 
 
 def test_norm():
@@ -131,6 +133,7 @@ def test_grouped_alone():
     assert grouped(T=-1) == wq.EINVAL
     assert grouped(E=-1) == wq.EINVAL
     assert grouped(R=None) == wq.EINVAL             # M != T without rows
+    assert grouped(M=0) == wq.EINVAL                # rows of no source
     assert grouped(M=1 << 20, K=4096) == wq.EUNSUPPORTED
     assert grouped(E=(1 << 20) + 1) == wq.EUNSUPPORTED
     assert grouped(T=0, O=None) == wq.OK

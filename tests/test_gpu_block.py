@@ -321,6 +321,30 @@ def test_grouped_edges():
     assert np.array_equal(y[keep], want[keep])
 
 
+@pytest.mark.parametrize("counts", [[3, 4], [40, 30, 0, 60]])
+def test_rows_without_a_source_are_zero_beside_nan(counts):
+    """A row index outside the source reads zeros, whatever scales row 0 has."""
+    case(f"grouped rows without a source {counts}")
+    N, K, E = 136, 272, len(counts)
+    off, rows = groups(counts, 1, 9)
+    rows[rows == 0] = 1
+    rows[::3] = np.resize([-1, 9, 1 << 30], rows[::3].shape)
+    xq, xs = block.quantize_act(up(rows_bits(9, K, 1)))
+    q = weight(N, K, 2, E)
+    xs[0] = float("nan")
+    y = host(block.grouped_linear(xq, xs, q, torch.from_numpy(off).to(DEV), rows=torch.from_numpy(rows).to(DEV)))
+    assert (y[::3] & 0x7FFF == 0).all() and np.isfinite(C.bf16_to_f32(y)).all()
+
+
+def test_grouped_over_many_experts():
+    """More experts than a wave's 64 lanes, the last ones in reach of every row tile."""
+    case("grouped over 1000 experts")
+    E, N, K = 1000, 40, 144
+    counts = np.zeros(E, np.int64)
+    counts[[0, 63, 64, 127, 500, 998, 999]] = [3, 1, 20, 2, 17, 1, 5]
+    check_grouped(list(counts), N, K, 12, 21)
+
+
 def test_weights_past_32_bit_offsets():
     """More than 2^32 bytes of weights: the last expert's product."""
     E, N, K = 67, 2048, 32768

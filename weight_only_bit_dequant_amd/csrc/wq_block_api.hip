@@ -13,6 +13,9 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxGrid = 65535;  // workgroups along y and z
+// Scale blocks of a row operator's result: at most 32 threads for each (64 for
+// a row of one), and a launch holds fewer than 2^32.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 27;
 
 wq_status fail(wq_status st, const char* fmt, ...) {
   char text[256];
@@ -24,6 +27,7 @@ wq_status fail(wq_status st, const char* fmt, ...) {
 }
 
 wq_status launched(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration) return fail(WQ_EUNSUPPORTED, "%s: more tiles than a launch holds", what);
   return e == hipSuccess ? wq::api_ok() : fail(WQ_EHIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
@@ -49,7 +53,7 @@ wq_status quant_rows(const char* what, bool gate, const void* X, int64_t ldx, in
   if (ldx % 8) return fail(WQ_EALIGN, "%s: row stride %lld is not a multiple of 8", what, (long long)ldx);
   if (!aligned(X, 16) || !aligned(Xq, 16)) return fail(WQ_EALIGN, "%s: input and codes must be 16-byte aligned", what);
   if (!aligned(Xs, 4)) return fail(WQ_EALIGN, "%s: scales must be 4-byte aligned", what);
-  if (M * blocks(K) >= (int64_t)1 << 31) return fail(WQ_EUNSUPPORTED, "%s: 2^31 scale blocks or more", what);
+  if (M * blocks(K) >= kMaxBlocks) return fail(WQ_EUNSUPPORTED, "%s: 2^27 scale blocks or more", what);
   return launched(wq::launch_block_quant_rows(gate, (const uint16_t*)X, ldx, M, K, (uint8_t*)Xq, Xs,
                                               (hipStream_t)stream),
                   what);
@@ -116,6 +120,7 @@ wq_status wq_block_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* 
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(WQ_EINVAL, "%s: eps must be finite and not negative", what);
   if (K > wq::kNormMaxK) return fail(WQ_EUNSUPPORTED, "%s: K above %lld", what, (long long)wq::kNormMaxK);
   if (M == 0 || K == 0) return wq::api_ok();
+  if (M * (blocks(K) > 1 ? blocks(K) : 2) >= kMaxBlocks) return fail(WQ_EUNSUPPORTED, "%s: 2^27 scale blocks or more", what);
   if (!X || !gain || !Xq || !Xs) return fail(WQ_EINVAL, "%s: null pointer", what);
   if (ldx < K) return fail(WQ_EINVAL, "%s: row stride %lld is shorter than a row", what, (long long)ldx);
   if (ldx % 8) return fail(WQ_EALIGN, "%s: row stride %lld is not a multiple of 8", what, (long long)ldx);
@@ -172,6 +177,7 @@ wq_status wq_block_grouped_linear(const void* Xq, const float* Xs, int64_t M, in
   if (!offsets) return fail(WQ_EINVAL, "%s: null offsets", what);
   if (!aligned(offsets, 4) || !aligned(rows, 4))
     return fail(WQ_EALIGN, "%s: offsets and rows must be 4-byte aligned", what);
+  if (M == 0) return fail(WQ_EINVAL, "%s: %lld rows from none", what, (long long)T);
   if (!rows && M != T) return fail(WQ_EINVAL, "%s: without rows M must be T (M=%lld T=%lld)", what, (long long)M, (long long)T);
   if (rows && M * K >= (int64_t)1 << 32) return fail(WQ_EUNSUPPORTED, "%s: 2^32 codes or more behind rows", what);
   wq::BlockGemmArgs a{};

@@ -57,6 +57,19 @@ __device__ __forceinline__ int xcd_order(int G) {
   return x * q + min(x, r) + (b >> 3);
 }
 
+// Inclusive sum over the lanes: shifts within rows of 16, then each row's last
+// lane to the next row and the first half's to the second (DPP row_shr and
+// row_bcast; a lane without a source adds 0).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 // Row tile `ti` of the experts' row tiles, BM rows each, numbered through all
 // experts: expert e (-1: no such tile), its rows [t0, end).  Offsets are
 // clamped to [0, T].  Every lane of the wave gets the same answer.
@@ -74,12 +87,7 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* off, int E, int T, in
       hi = min(max(off[e + 1], lo), T);
     }
     const int tiles = (hi - lo + BM - 1) / BM;
-    int upto = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
+    const int upto = wave_scan(tiles);
     const int first = before + upto - tiles;
     const uint64_t hit = __ballot(ti >= first && ti < first + tiles);
     if (hit) {
@@ -200,7 +208,7 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
     for (int j = 0; j < MT; ++j) {
       av[j] = load_scales<kRun>(sa[j] + first, KB);
 #pragma unroll
-      for (int u = 0; u < kRun; ++u) av[j].v[u] *= bv.v[u];
+      for (int u = 0; u < kRun; ++u) av[j].v[u] = (uint32_t)src[j] < (uint32_t)a.M ? av[j].v[u] * bv.v[u] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kRun; ++u) {
@@ -646,17 +654,22 @@ static int64_t row_tiles(const BlockGemmArgs& a, int64_t bm) {
   return (a.T + (int64_t)(a.E < a.T ? a.E : a.T) * (bm - 1)) / bm;
 }
 
+// A launch holds fewer than 2^32 threads (and its workgroups are numbered by ints).
+static bool too_many(int64_t groups, int threads) { return groups >= ((int64_t)1 << 32) / threads || groups >= INT32_MAX; }
+
 template <int BN, int BM, int WN, int WM, int NS, int KS>
 static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   using T = TileT<BN, BM, WN, WM, NS, KS>;
   static_assert(T::SMEM <= 160 * 1024, "LDS of a CU");
+  constexpr int threads = KS * WN * WM * 64;
+  const int64_t gx = (a.N + BN - 1) / BN, gy = row_tiles(a, BM);
+  if (too_many(gx * gy, threads)) return hipErrorInvalidConfiguration;
   static std::atomic<int> allowed[2];
   const bool tail = a.K % 128 != 0;
   const auto kern = tail ? k_block_tile<BN, BM, WN, WM, NS, KS, true> : k_block_tile<BN, BM, WN, WM, NS, KS, false>;
   hipError_t e = allow_smem(kern, T::SMEM, allowed[tail]);
   if (e != hipSuccess) return e;
-  const int64_t gx = (a.N + BN - 1) / BN, gy = row_tiles(a, BM);
-  kern<<<(unsigned)(gx * gy), KS * WN * WM * 64, T::SMEM, s>>>(a, (int)gx, (int)gy);
+  kern<<<(unsigned)(gx * gy), threads, T::SMEM, s>>>(a, (int)gx, (int)gy);
   return hipGetLastError();
 }
 
@@ -665,50 +678,59 @@ static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
   constexpr int smem = StreamT<NT, MT, W>::SMEM;
   static_assert(smem <= 65536, "no leave needed for the LDS size");
   const int64_t gx = (a.N + 16 * NT - 1) / (16 * NT), gy = row_tiles(a, 16 * MT);
+  if (too_many(gx * gy, W * 64)) return hipErrorInvalidConfiguration;
   k_block_stream<NT, MT, W><<<(unsigned)(gx * gy), W * 64, smem, s>>>(a, (int)gx, (int)gy);
   return hipGetLastError();
 }
 
+// Tile forms, with the time of one scale block of K for a round of 256 tiles, one to a CU (us; measured at N = K =
+// 4096, 32 blocks: 63, 37, 24, 15 and 11 us for the whole call).
+struct Form {
+  int bn, bm;
+  float per_block;
+  hipError_t (*launch)(const BlockGemmArgs&, hipStream_t);
+};
+static const Form kForms[] = {{256, 256, 1.85f, tile_launch<256, 256, 2, 4, 2, 1>},
+                              {256, 128, 1.05f, tile_launch<256, 128, 4, 2, 3, 1>},
+                              {128, 128, 0.62f, tile_launch<128, 128, 2, 4, 4, 1>},
+                              {128, 64, 0.34f, tile_launch<128, 64, 2, 2, 3, 2>},
+                              {64, 64, 0.24f, tile_launch<64, 64, 2, 2, 4, 2>}};
+
 // Which form.  Times in us, of graphs of back-to-back launches.
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
-  if (a.offsets) {
-    // By an expert's rows on average.  Few: the weights are streamed, 64 columns to a workgroup, so that fewer of
-    // them look for their rows (64 rows of 32 experts, 2048 x 2048: 17 against 24 with 16 columns and 22 with
-    // 256 x 128 tiles; 16 rows each: 26 against 39).  More: wide tiles, again to have few workgroups (31 rows each,
-    // 64 experts 1536 x 2048: 46 against 52 streamed; 62 rows each, 2048 x 2048: 41 against 44 with 64 x 64 tiles
-    // and 54 streamed); 256 rows to a tile from 512 on (172 against 173 at 1024, less traffic).
-    const int rows = (a.T + a.E - 1) / a.E;
-    if (rows <= 16) return stream_launch<4, 1, 4>(a, s);
-    if (rows < 512) return tile_launch<256, 128, 4, 2, 3, 1>(a, s);
-    return tile_launch<256, 256, 2, 4, 2, 1>(a, s);
-  }
-  if (a.M <= 64) {
-    // Streamed.  Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best with
-    // the smallest workgroups' tiles (1 x 4096 x 3072: 4.7 against 5.9 with 32 columns), many share what they read
-    // (32 x 8192 x 8192: 13.1 against 16.2 with 16 columns; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
-    const int64_t tiles = ((a.N + 15) / 16) * (int64_t)((a.M + 15) / 16);
+  const int groups = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
+  const int rows = (a.T + groups - 1) / groups;  // of an expert, on average (a.M for a plain Linear)
+  // Few rows: streamed.  Experts: 64 columns to a workgroup, so that fewer of them look for their rows (64 rows of
+  // 32 experts, 2048 x 2048: 17 against 24 with 16 columns and 22 with 256 x 128 tiles; 16 rows each: 26 against 39).
+  if (a.offsets && rows <= 16) return stream_launch<4, 1, 4>(a, s);
+  if (!a.offsets && rows <= 64) {
+    // Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best one to a
+    // workgroup (1 x 4096 x 3072: 4.7 against 5.9 with two), many share what they read (32 x 8192 x 8192: 13.1
+    // against 16.2; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
+    const int64_t tiles = ((a.N + 15) / 16) * (int64_t)((rows + 15) / 16);
     if (tiles <= 512) return stream_launch<1, 1, 8>(a, s);
-    if (tiles <= 1024 || a.M <= 16) return stream_launch<2, 1, 4>(a, s);
+    if (tiles <= 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<2, 2, 4>(a, s);
   }
-  // Tiles: the form with the least time for its rounds of 256 workgroups, from each form's time for one scale
-  // block of K (measured at N = K = 4096, 32 blocks, one full round of tiles: 65, 37, 24, 15 and 11 us in all).
-  struct Form {
-    int bn, bm;
-    float per_block;  // us
-    hipError_t (*launch)(const BlockGemmArgs&, hipStream_t);
+  auto tiles = [&](const Form& f) {
+    return ((a.N + f.bn - 1) / f.bn) * (int64_t)groups * ((rows + f.bm - 1) / f.bm);
   };
-  static const Form forms[] = {{256, 256, 1.95f, tile_launch<256, 256, 2, 4, 2, 1>},
-                               {256, 128, 1.05f, tile_launch<256, 128, 4, 2, 3, 1>},
-                               {128, 128, 0.62f, tile_launch<128, 128, 2, 4, 4, 1>},
-                               {128, 64, 0.34f, tile_launch<128, 64, 2, 2, 3, 2>},
-                               {64, 64, 0.24f, tile_launch<64, 64, 2, 2, 4, 2>}};
   const Form* best = nullptr;
-  float least = 0.f;
-  for (const Form& f : forms) {
-    const int64_t tiles = ((a.N + f.bn - 1) / f.bn) * (int64_t)((a.M + f.bm - 1) / f.bm);
-    const float t = (float)((tiles + 255) / 256) * f.per_block;
-    if (!best || t < least) best = &f, least = t;
+  if (a.offsets && rows < 256) {
+    // The weights' stream bounds these: the widest form that fills the chip (31 rows each of 64 experts, 1536 x 2048:
+    // 45 with 256 x 128 tiles against 52-56 with the others; 62 and 125 rows each of 32, 2048 x 2048: 41 and 45
+    // against 44 and 57; 37 rows each of 8, 4096 x 4096, 128 wide tiles: 43 against 39 with 128 x 64).
+    for (int f : {1, 3, 4}) {
+      best = &kForms[f];
+      if (tiles(*best) >= 192) break;
+    }
+  } else {
+    // the least time for the rounds
+    float least = 0.f;
+    for (const Form& f : kForms) {
+      const float t = (float)((tiles(f) + 255) / 256) * f.per_block;
+      if (!best || t < least) best = &f, least = t;
+    }
   }
   return best->launch(a, s);
 }

@@ -11,6 +11,8 @@ Each page quantizes a model in place and then calls it:
     the page title's "Dynamic Activation + MX Weight" config)
   * Static FP8 page, "Calibrate, then insert static FP8 Q/DQ":
     ``quantize_static_fp8(model, (example_input,), calibration_steps=10)``
+  * block-scaled FP8 (a scale for each 128 codes; no page):
+    ``quantize_linear_fp8_block(model)``
 
 Every ``nn.Linear`` in the model is replaced by a module that holds the packed
 weight and runs the library's kernels in ``forward``; the weight is packed once
@@ -19,7 +21,7 @@ and never refit.  Modules run on the GPU only: there is no CPU path.
 
 import torch
 
-from . import wq
+from . import block, wq
 
 _CODES = {"int4": "int4", "nvfp4": "nvfp4", "fp8": "fp8", "mxfp4": "mxfp4"}
 
@@ -91,6 +93,23 @@ class StaticFP8Linear(torch.nn.Module):
         return y.reshape(*lead, self.out_features)
 
 
+class BlockFP8Linear(torch.nn.Module):
+    """Block-scaled FP8 Linear: activations quantized on every call with a scale
+    for each 128 of a row, weights with one for each 128 x 128 block, the product
+    on the FP8 matrix cores (``wq_block_quantize_act``, ``wq_block_linear``)."""
+
+    def __init__(self, linear):
+        super().__init__()
+        self.in_features, self.out_features = linear.in_features, linear.out_features
+        self.q = block.quantize_weight(linear.weight.detach().to(torch.bfloat16).contiguous())
+        self.bias = _bias(linear)
+
+    def forward(self, x):
+        x2, lead = _as_2d(x)
+        y = block.linear(*block.quantize_act(x2), self.q, self.bias)
+        return y.reshape(*lead, self.out_features)
+
+
 def _swap(model, make):
     """Replace every nn.Linear under `model` (in place) by make(linear, name)."""
     if isinstance(model, torch.nn.Linear):
@@ -121,6 +140,10 @@ def quantize_linear_mxfp4(model, dynamic_activation=False):
     if dynamic_activation:
         return _swap(model, lambda lin, _: MXDynamicLinear(lin))
     return _swap(model, lambda lin, _: QuantizedLinear(lin, "mxfp4"))
+
+
+def quantize_linear_fp8_block(model):
+    return _swap(model, lambda lin, _: BlockFP8Linear(lin))
 
 
 @torch.no_grad()
