@@ -669,8 +669,7 @@ static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   const auto kern = tail ? k_block_tile<BN, BM, WN, WM, NS, KS, true> : k_block_tile<BN, BM, WN, WM, NS, KS, false>;
   hipError_t e = allow_smem(kern, T::SMEM, allowed[tail]);
   if (e != hipSuccess) return e;
-  kern<<<(unsigned)(gx * gy), threads, T::SMEM, s>>>(a, (int)gx, (int)gy);
-  return hipGetLastError();
+  return launch(kern, dim3((unsigned)(gx * gy)), threads, T::SMEM, s, a, (int)gx, (int)gy);
 }
 
 template <int NT, int MT, int W>
@@ -679,8 +678,7 @@ static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
   static_assert(smem <= 65536, "no leave needed for the LDS size");
   const int64_t gx = (a.N + 16 * NT - 1) / (16 * NT), gy = row_tiles(a, 16 * MT);
   if (too_many(gx * gy, W * 64)) return hipErrorInvalidConfiguration;
-  k_block_stream<NT, MT, W><<<(unsigned)(gx * gy), W * 64, smem, s>>>(a, (int)gx, (int)gy);
-  return hipGetLastError();
+  return launch(k_block_stream<NT, MT, W>, dim3((unsigned)(gx * gy)), W * 64, smem, s, a, (int)gx, (int)gy);
 }
 
 // Tile forms, with the time of one scale block of K for a round of 256 tiles, one to a CU (us; measured at N = K =
@@ -705,11 +703,13 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
   if (a.offsets && rows <= 16) return stream_launch<4, 1, 4>(a, s);
   if (!a.offsets && rows <= 64) {
     // Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best one to a
-    // workgroup (1 x 4096 x 3072: 4.7 against 5.9 with two), many share what they read (32 x 8192 x 8192: 13.1
-    // against 16.2; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
+    // workgroup (1 x 4096 x 3072: 4.7 against 5.1 with two, 32 x 2048 x 2048: 3.6 against 4.2), many share what they
+    // read (32 x 4096 x 3072: 5.4 against 5.9; 32 x 8192 x 8192: 13.1 with four waves, 14.4 with eight, 16.2 with 16
+    // columns; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
     const int64_t tiles = ((a.N + 15) / 16) * (int64_t)((rows + 15) / 16);
-    if (tiles <= 512) return stream_launch<1, 1, 8>(a, s);
-    if (tiles <= 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
+    if (tiles < 512) return stream_launch<1, 1, 8>(a, s);
+    if (tiles < 1024) return stream_launch<2, 1, 8>(a, s);
+    if (tiles == 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<2, 2, 4>(a, s);
   }
   auto tiles = [&](const Form& f) {

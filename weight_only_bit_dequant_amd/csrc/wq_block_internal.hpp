@@ -18,6 +18,17 @@ constexpr int kBlk = 128;  // K elements (and weight rows) per scale
 wq_status api_error(wq_status st, const char* message);
 wq_status api_ok();
 
+// Enqueue a kernel.  (hipLaunchKernel itself: the <<<>>> form first stores the
+// configuration and takes it back, 0.25 of its 3.65 us on the host.)
+template <typename... P, typename... A>
+hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, hipStream_t s, const A&... a) {
+  static_assert(sizeof...(P) == sizeof...(A), "one argument for each parameter");
+  return [&](P... p) {
+    void* args[] = {(void*)&p...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, smem, s);
+  }(a...);
+}
+
 constexpr int64_t kNormMaxK = 32768;  // 16 waves x 64 lanes x 4 chunks of 8
 
 struct BlockNormArgs {

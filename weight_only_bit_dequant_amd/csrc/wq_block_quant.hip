@@ -252,41 +252,36 @@ hipError_t launch_block_quant_rows(bool gate, const uint16_t* X, int64_t ldx, in
     while ((2u << sh) < KB) ++sh;
     magic = (uint32_t)((((uint64_t)1 << (32 + sh)) + KB - 1) / KB);
   }
-  if (gate)
-    k_block_quant_rows<true><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, magic, sh, (uint32_t)K, Xq, Xs);
-  else
-    k_block_quant_rows<false><<<grid, 256, 0, s>>>(X, ldx, nblk, KB, magic, sh, (uint32_t)K, Xq, Xs);
-  return hipGetLastError();
+  return launch(gate ? k_block_quant_rows<true> : k_block_quant_rows<false>, dim3(grid), 256, 0, s, X, ldx, nblk, KB, magic,
+                sh, (uint32_t)K, Xq, Xs);
 }
 
 template <int WPR, int CPT>
-static void norm_launch(const BlockNormArgs& a, hipStream_t s) {
+static hipError_t norm_launch(const BlockNormArgs& a, hipStream_t s) {
   constexpr int rows = norm_rows<WPR>();
-  k_block_norm<WPR, CPT><<<(unsigned)((a.M + rows - 1) / rows), rows * WPR * 64, 0, s>>>(a);
+  return launch(k_block_norm<WPR, CPT>, dim3((unsigned)((a.M + rows - 1) / rows)), rows * WPR * 64, 0, s, a);
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
   // The narrowest form that holds a row, more waves before more chunks: a row of 8192 in 8 waves x 2 chunks takes
   // 163 us against 166 in 4 x 4 and 179 in 16 x 1 (16384 rows), 3.7 against 4.3 us (64 rows).
   const int chunks = (a.K + 127) / 128 * 16;  // whole 16-lane rows
-  if (chunks <= 64) norm_launch<1, 1>(a, s);
-  else if (chunks <= 128) norm_launch<2, 1>(a, s);
-  else if (chunks <= 192) norm_launch<3, 1>(a, s);
-  else if (chunks <= 256) norm_launch<4, 1>(a, s);
-  else if (chunks <= 384) norm_launch<6, 1>(a, s);
-  else if (chunks <= 512) norm_launch<4, 2>(a, s);
-  else if (chunks <= 768) norm_launch<6, 2>(a, s);
-  else if (chunks <= 1024) norm_launch<8, 2>(a, s);
-  else if (chunks <= 2048) norm_launch<8, 4>(a, s);
-  else norm_launch<16, 4>(a, s);
-  return hipGetLastError();
+  if (chunks <= 64) return norm_launch<1, 1>(a, s);
+  if (chunks <= 128) return norm_launch<2, 1>(a, s);
+  if (chunks <= 192) return norm_launch<3, 1>(a, s);
+  if (chunks <= 256) return norm_launch<4, 1>(a, s);
+  if (chunks <= 384) return norm_launch<6, 1>(a, s);
+  if (chunks <= 512) return norm_launch<4, 2>(a, s);
+  if (chunks <= 768) return norm_launch<6, 2>(a, s);
+  if (chunks <= 1024) return norm_launch<8, 2>(a, s);
+  if (chunks <= 2048) return norm_launch<8, 4>(a, s);
+  return norm_launch<16, 4>(a, s);
 }
 
 hipError_t launch_block_quant_weight(const uint16_t* W, int64_t E, int64_t N, int64_t K, uint8_t* codes,
                                      float* scales, hipStream_t s) {
   const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128), (unsigned)E);
-  k_block_quant_weight<<<grid, 256, 0, s>>>(W, (int)N, (int)K, codes, scales);
-  return hipGetLastError();
+  return launch(k_block_quant_weight, grid, 256, 0, s, W, (int)N, (int)K, codes, scales);
 }
 
 }  // namespace wq
