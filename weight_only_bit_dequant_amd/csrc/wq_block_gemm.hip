@@ -6,6 +6,8 @@
 // and adds to the fp32 sum (one fused multiply-add per output and block).  The
 // weights are operand A, so a lane's four results are four columns n of one
 // row m: one activation scale, one weight scale, 8 bytes of bf16 output.
+#include <cmath>
+
 #include "wq_block_internal.hpp"
 #include "wq_kernel_common.hpp"
 
@@ -70,35 +72,53 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Row tile `ti` of the experts' row tiles, BM rows each, numbered through all
-// experts: expert e (-1: no such tile), its rows [t0, end).  Offsets are
-// clamped to [0, T].  Every lane of the wave gets the same answer.
+// The experts' row tiles, BM rows each, numbered through all experts; lane l
+// holds expert e0 + l of a stretch of 64.  Offsets are clamped to [0, T].
 struct RowTile {
-  int e, t0, end;
+  int e, t0, end;  // expert, its rows [t0, end) of this tile and after
 };
-__device__ __forceinline__ RowTile row_tile(const int32_t* off, int E, int T, int BM, int ti) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;  // tiles of the experts before this stretch of 64
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
+struct RowTiles {
+  const int32_t* off;
+  int E, T, BM;
+  int lo, hi, first, tiles, total;  // the first stretch; all tiles
+
+  // lane's expert of a stretch whose tiles come after `before` others; returns the number up to its end
+  __device__ __forceinline__ int stretch(int e0, int before, int& l, int& h, int& f, int& n) const {
+    const int e = e0 + (int)(threadIdx.x & 63);
+    l = h = 0;
     if (e < E) {
-      lo = min(max(off[e], 0), T);
-      hi = min(max(off[e + 1], lo), T);
+      l = min(max(off[e], 0), T);
+      h = min(max(off[e + 1], l), T);
     }
-    const int tiles = (hi - lo + BM - 1) / BM;
-    const int upto = wave_scan(tiles);
-    const int first = before + upto - tiles;
-    const uint64_t hit = __ballot(ti >= first && ti < first + tiles);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const int elo = __builtin_amdgcn_readlane(lo, l), ehi = __builtin_amdgcn_readlane(hi, l);
-      return {e0 + l, elo + (ti - __builtin_amdgcn_readlane(first, l)) * BM, ehi};
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
+    n = (h - l + BM - 1) / BM;
+    const int upto = wave_scan(n);
+    f = before + upto - n;
+    return before + __builtin_amdgcn_readlane(upto, 63);
   }
-  return {-1, 0, 0};
-}
+  __device__ __forceinline__ RowTiles(const int32_t* o, int experts, int rows, int bm) : off(o), E(experts), T(rows), BM(bm) {
+    total = stretch(0, 0, lo, hi, first, tiles);
+    for (int e0 = 64; e0 < E; e0 += 64) {
+      int l, h, f, n;
+      total = stretch(e0, total, l, h, f, n);
+    }
+  }
+  // tile ti < total; every lane of the wave gets the same answer
+  __device__ __forceinline__ RowTile find(int ti) const {
+    int l = lo, h = hi, f = first, n = tiles;
+    for (int e0 = 0;;) {
+      const uint64_t hit = __ballot(ti >= f && ti < f + n);
+      if (hit) {
+        const int at = __builtin_ctzll(hit);
+        return {e0 + at, __builtin_amdgcn_readlane(l, at) + (ti - __builtin_amdgcn_readlane(f, at)) * BM,
+                __builtin_amdgcn_readlane(h, at)};
+      }
+      const int before = __builtin_amdgcn_readlane(f, 63) + __builtin_amdgcn_readlane(n, 63);
+      e0 += 64;
+      if (e0 >= E) return {0, 0, 0};  // not reached for ti < total
+      stretch(e0, before, l, h, f, n);
+    }
+  }
+};
 
 // LDS slot of 16-byte chunk k of row r: the four lane groups' reads of 16 rows
 // then fall on distinct banks.
@@ -132,11 +152,18 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
   // consecutive workgroups of an XCD take the row tiles of one column tile, which share its weights
-  const int tile = xcd_order(gx * gy), tx = tile / gy, ty = tile - tx * gy;
-  RowTile t{0, ty * 16 * MT, a.M};
+  RowTile t;
+  int tx;
   if (a.offsets) {
-    t = row_tile(a.offsets, a.E, a.T, 16 * MT, ty);
-    if (t.e < 0) return;
+    const RowTiles all(a.offsets, a.E, a.T, 16 * MT);
+    if ((int)blockIdx.x >= gx * all.total) return;  // the grid is for a bound on their number
+    const int tile = xcd_order(gx * all.total);
+    tx = tile / all.total;
+    t = all.find(tile - tx * all.total);
+  } else {
+    const int tile = xcd_order(gx * gy), ty = tile % gy;
+    tx = tile / gy;
+    t = {0, ty * 16 * MT, a.M};
   }
   const int n0 = tx * 16 * NT;
 
@@ -336,17 +363,22 @@ __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs
 
   // bands of 4 column tiles, row tile by row tile: tiles in flight on one XCD
   // share operands both ways
-  int tx, ty;
-  {
-    const int idx = xcd_order(gx * gy);
-    const int band = idx / (4 * gy), in = idx - band * 4 * gy, wide = min(4, gx - 4 * band);
-    ty = in / wide;
+  int tx;
+  auto place = [&](int rows) {  // of so many row tiles: this workgroup's
+    const int idx = xcd_order(gx * rows);
+    const int band = idx / (4 * rows), in = idx - band * 4 * rows, wide = min(4, gx - 4 * band), ty = in / wide;
     tx = 4 * band + in - ty * wide;
-  }
-  RowTile t{0, ty * BM, a.M};
+    return ty;
+  };
+  RowTile t;
   if (a.offsets) {
-    t = row_tile(a.offsets, a.E, a.T, BM, ty);
-    if (t.e < 0) return;
+    // the tiles there are, not the bound that the grid is for: the XCDs share them out evenly (5604 rows of 16
+    // experts, 3424 x 3072: 111 us by the bound)
+    const RowTiles all(a.offsets, a.E, a.T, BM);
+    if ((int)blockIdx.x >= gx * all.total) return;
+    t = all.find(place(all.total));
+  } else {
+    t = {0, place(gy) * BM, a.M};
   }
   const int n0 = tx * BN;
 
@@ -681,18 +713,20 @@ static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
   return launch(k_block_stream<NT, MT, W>, dim3((unsigned)(gx * gy)), W * 64, smem, s, a, (int)gx, (int)gy);
 }
 
-// Tile forms, with the time of one scale block of K for a round of 256 tiles, one to a CU (us; measured at N = K =
-// 4096, 32 blocks: 63, 37, 24, 15 and 11 us for the whole call).
+// Forms for many rows, widest first.  Time of a launch in us: 2.5 + rounds (start + blocks per_block), a round being
+// `at_once` tiles.  Fitted to N = 4096 with M of one full round at 32 scale blocks of K and M = 4096 at 4 (us: 63 and
+// 16.5, 36.5 and 18.3, 23.7 and 21.9, 14.9 and 37, 11.3 and 54, 16.6 and 28.5); other shapes came within 20 % of it.
 struct Form {
-  int bn, bm;
-  float per_block;
+  int bn, bm, at_once;
+  float start, per_block;
   hipError_t (*launch)(const BlockGemmArgs&, hipStream_t);
 };
-static const Form kForms[] = {{256, 256, 1.85f, tile_launch<256, 256, 2, 4, 2, 1>},
-                              {256, 128, 1.05f, tile_launch<256, 128, 4, 2, 3, 1>},
-                              {128, 128, 0.62f, tile_launch<128, 128, 2, 4, 4, 1>},
-                              {128, 64, 0.34f, tile_launch<128, 64, 2, 2, 3, 2>},
-                              {64, 64, 0.24f, tile_launch<64, 64, 2, 2, 4, 2>}};
+static const Form kForms[] = {{256, 256, 256, 7.4f, 1.66f, tile_launch<256, 256, 2, 4, 2, 1>},
+                              {256, 128, 256, 3.6f, 0.96f, tile_launch<256, 128, 4, 2, 3, 1>},
+                              {128, 128, 256, 2.5f, 0.58f, tile_launch<128, 128, 2, 4, 4, 1>},
+                              {128, 64, 256, 3.1f, 0.29f, tile_launch<128, 64, 2, 2, 3, 2>},
+                              {64, 64, 256, 2.4f, 0.20f, tile_launch<64, 64, 2, 2, 4, 2>},
+                              {64, 64, 512, 1.7f, 0.39f, tile_launch<64, 64, 2, 2, 4, 1>}};
 
 // Which form.  Times in us, of graphs of back-to-back launches.
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
@@ -712,26 +746,29 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
     if (tiles == 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<2, 2, 4>(a, s);
   }
-  auto tiles = [&](const Form& f) {
-    return ((a.N + f.bn - 1) / f.bn) * (int64_t)groups * ((rows + f.bm - 1) / f.bm);
+  // More rows: the form with the least time, but no less than the memory's (weights, for experts those of all that
+  // have rows), where the widest does best: fewer workgroups look for their rows (31 rows each of 64 experts, 1536 x
+  // 2048: 45 with 256 x 128 tiles against 52-56 with the others).
+  const float blocks = (float)((a.K + 127) / 128), memory = 2.5f + (float)a.N * (float)a.K * (float)groups / 4.8e6f;
+  auto tiles = [&](int bn, int bm) {  // an expert's last row tile is half full on average
+    const float m = a.offsets ? (float)rows / (float)bm + 0.5f : (float)((rows + bm - 1) / bm);
+    return (float)((a.N + bn - 1) / bn) * (float)groups * (m > 1.f ? m : 1.f);
   };
   const Form* best = nullptr;
-  if (a.offsets && rows < 256) {
-    // The weights' stream bounds these: the widest form that fills the chip (31 rows each of 64 experts, 1536 x 2048:
-    // 45 with 256 x 128 tiles against 52-56 with the others; 62 and 125 rows each of 32, 2048 x 2048: 41 and 45
-    // against 44 and 57; 37 rows each of 8, 4096 x 4096, 128 wide tiles: 43 against 39 with 128 x 64).
-    for (int f : {1, 3, 4}) {
-      best = &kForms[f];
-      if (tiles(*best) >= 192) break;
-    }
-  } else {
-    // the least time for the rounds
-    float least = 0.f;
-    for (const Form& f : kForms) {
-      const float t = (float)((tiles(f) + 255) / 256) * f.per_block;
-      if (!best || t < least) best = &f, least = t;
-    }
+  float least = 0.f;
+  for (const Form& f : kForms) {
+    const float n = tiles(f.bn, f.bm), rounds = ceilf(n / (float)f.at_once);
+    // (two tiles share a CU only when there are more than 256)
+    const float per = f.at_once == 512 && n <= 256.f ? 0.25f : f.per_block;
+    const float t = fmaxf(2.5f + rounds * (f.start + blocks * per), memory);
+    if (!best || t < 0.97f * least) best = &f, least = t;
   }
+  // The stream of 32 x 32 tiles keeps the chip filled where those are too few: 142 x 1224 x 3120 6.2 against 11.0,
+  // 94 x 2795 x 6144 11.1 against 14.8, 128 x 4096 x 4096 9.8 against 10.6; 256 x 4096 x 4096 16.7 against 11.3,
+  // 697 x 1512 x 640 8.5 against 6.6.
+  const float n = tiles(32, 32);
+  const float t = fmaxf(3.0f + 0.0045f * fmaxf(0.f, n - 300.f) + blocks * (0.09f + 0.00022f * n), memory);
+  if (t < 0.97f * least) return stream_launch<2, 2, 4>(a, s);
   return best->launch(a, s);
 }
 
