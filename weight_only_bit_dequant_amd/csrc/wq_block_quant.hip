@@ -76,8 +76,8 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
 }
 
 // silu(g) u = g / (1 + exp(-g)) u within a few fp32 ulp.
-//   exp(-g) = 2^t, t = -g log2 e in two parts: the high part's power comes from
-//   the hardware's 2^x, the low part enters as 1 + low ln 2;
+//   exp(-g) = 2^t, t = -g log2 e in two parts, the hardware's 2^x for what is
+//   left of them beside a whole number;
 //   the quotient is g' r with one correction by its remainder, r the hardware's
 //   reciprocal of d' (1 ulp).  d' = 2^-8 (1 + exp(-g)) and g' = 2^-8 g: r stays a
 //   normal number up to the largest d (reciprocals below 2^-126 read as 0).
@@ -86,17 +86,19 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
 // Two library calls (expf and division) took 45 instructions an element, more
 // than the memory's time (8192 x 8192: 75 us; its 335 MB at 5.7 TB/s: 59 us).
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  constexpr float L = -1.4426950216293335f, Ll = -1.9259629911e-8f, ln2 = 0.69314718056f;  // -log2 e = L + Ll
+  constexpr float L = -1.4426950216293335f, Ll = -1.9259629911e-8f;  // -log2 e = L + Ll
   constexpr float far = -88.6f;
   const float x = __builtin_amdgcn_fmed3f(g, far, 90.0f);
   const float hi = x * L;
   const float lo = __builtin_fmaf(x, Ll, __builtin_fmaf(x, L, -hi));
-  float e = __builtin_amdgcn_exp2f(hi);
-  e = __builtin_fmaf(e, lo * ln2, e);
+  const float whole = __builtin_rintf(hi);
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f((hi - whole) + lo), (int)whole);
   const float d = __builtin_fmaf(e, 0.00390625f, 0.00390625f), n = g * 0.00390625f;
   const float r = __builtin_amdgcn_rcpf(d);
   const float q = n * r;
-  return (g < far ? -0.0f : __builtin_fmaf(__builtin_fmaf(-q, d, n), r, q)) * u;
+  float v = __builtin_fmaf(__builtin_fmaf(-q, d, n), r, q);
+  asm("" : "+v"(v));  // a select, not a branch around the quotient for each element
+  return (g < far ? -0.0f : v) * u;
 }
 
 // ---------------------------------------------------------------- activation rows, gated activation
