@@ -234,6 +234,26 @@ def test_linear_large(M, N, K):
     check_product(y, (host(xq), host(xs), host(q["codes"]), host(q["scales"])))
 
 
+@pytest.mark.parametrize("M,N,K", [(4300, 4096, 528), (1025, 8190, 528)])
+def test_linear_rest_of_a_round(M, N, K):
+    """A few tiles more than the chip holds at once, of each form that splits those: every output row and column piece."""
+    case(f"linear rest {M}x{N}x{K}")
+    xq, xs = block.quantize_act(up(rows_bits(M, K, M + K, spread=True)))
+    q = weight(N, K, N + K)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y = C.bf16_to_f32(host(block.linear(xq, xs, q, out=out))).astype(np.float64)
+    assert np.isfinite(y).all()
+    hx, hs, hw, hv = host(xq), host(xs), host(q["codes"]), host(q["scales"])
+    rows = np.unique(np.concatenate([np.arange(0, M, 16), np.arange(max(0, M - 140), M)]))
+    check_product(y[rows], (hx[rows], hs[rows], hw, hv))
+
+
+@pytest.mark.parametrize("counts,N", [([1000, 0, 1300, 2000], 4000), ([40, 700, 0, 290], 8192)])
+def test_grouped_rest_of_a_round(counts, N):
+    case(f"grouped rest {counts} {N}")
+    check_grouped(counts, N, 400, 900, 3)
+
+
 def test_linear_nan_codes_reach_their_row_and_column_only():
     case("linear NaN codes")
     M, N, K = 70, 200, 272

@@ -7,6 +7,7 @@
 // weights are operand A, so a lane's four results are four columns n of one
 // row m: one activation scale, one weight scale, 8 bytes of bf16 output.
 #include <cmath>
+#include <type_traits>
 
 #include "wq_block_internal.hpp"
 #include "wq_kernel_common.hpp"
@@ -52,10 +53,10 @@ __device__ __forceinline__ Scales<CH> load_scales(const float* p, int KB) {
   return s;
 }
 
-// Place of this workgroup in an order that the XCDs share out in contiguous
+// Place of workgroup b of G in an order that the XCDs share out in contiguous
 // pieces (workgroup b runs on XCD b % 8, and each XCD has its own L2).
-__device__ __forceinline__ int xcd_order(int G) {
-  const int b = blockIdx.x, q = G >> 3, r = G & 7, x = b & 7;
+__device__ __forceinline__ int xcd_order(int b, int G) {
+  const int q = G >> 3, r = G & 7, x = b & 7;
   return x * q + min(x, r) + (b >> 3);
 }
 
@@ -157,11 +158,11 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
   if (a.offsets) {
     const RowTiles all(a.offsets, a.E, a.T, 16 * MT);
     if ((int)blockIdx.x >= gx * all.total) return;  // the grid is for a bound on their number
-    const int tile = xcd_order(gx * all.total);
+    const int tile = xcd_order(blockIdx.x, gx * all.total);
     tx = tile / all.total;
     t = all.find(tile - tx * all.total);
   } else {
-    const int tile = xcd_order(gx * gy), ty = tile % gy;
+    const int tile = xcd_order(blockIdx.x, gx * gy), ty = tile % gy;
     tx = tile / gy;
     t = {0, ty * 16 * MT, a.M};
   }
@@ -326,8 +327,9 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
 // step before.
 constexpr int kScaleSteps = 8;
 
-template <int BN, int BM, int WN, int WM, int NS, int KS>
-struct TileT {
+template <int BN_, int BM_, int WN_, int WM_, int NS_, int KS_>
+struct Tile {
+  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, NS = NS_, KS = KS_, THREADS = KS * WN * WM * 64;
   static constexpr int WAVES = WN * WM, TN = BN / (16 * WN), TM = BM / (16 * WM);
   static constexpr int STAGE = (BN + BM) * 128;
   static constexpr int NB = BN / 128 ? BN / 128 : 1;  // 128-column blocks
@@ -346,9 +348,9 @@ struct TileT {
 
 // TAIL: K % 128 != 0, chunks past K read zeros.  (Without it the loads carry no
 // mask; those of steps past the end read the last block again, unused.)
-template <int BN, int BM, int WN, int WM, int NS, int KS, bool TAIL>
-__global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
-  using T = TileT<BN, BM, WN, WM, NS, KS>;
+template <class T, bool TAIL>
+__device__ __forceinline__ void tile(const BlockGemmArgs& a, const RowTile t, const int n0) {
+  constexpr int BN = T::BN, BM = T::BM, WN = T::WN, WM = T::WM, NS = T::NS, KS = T::KS;
   constexpr int TN = T::TN, TM = T::TM, W = T::WAVES;
   constexpr int LJW = BN / (8 * W), LJ = (BN + BM) / (8 * W);  // loads per wave and step: weights, all
   extern __shared__ __attribute__((aligned(16))) unsigned char shared[];
@@ -360,27 +362,6 @@ __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs
   const int g = lane >> 4, c = lane & 15;
   const int wn = wave % WN, wm = wave / WN;
   const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
-
-  // bands of 4 column tiles, row tile by row tile: tiles in flight on one XCD
-  // share operands both ways
-  int tx;
-  auto place = [&](int rows) {  // of so many row tiles: this workgroup's
-    const int idx = xcd_order(gx * rows);
-    const int band = idx / (4 * rows), in = idx - band * 4 * rows, wide = min(4, gx - 4 * band), ty = in / wide;
-    tx = 4 * band + in - ty * wide;
-    return ty;
-  };
-  RowTile t;
-  if (a.offsets) {
-    // the tiles there are, not the bound that the grid is for: the XCDs share them out evenly (5604 rows of 16
-    // experts, 3424 x 3072: 111 us by the bound)
-    const RowTiles all(a.offsets, a.E, a.T, BM);
-    if ((int)blockIdx.x >= gx * all.total) return;
-    t = all.find(place(all.total));
-  } else {
-    t = {0, place(gy) * BM, a.M};
-  }
-  const int n0 = tx * BN;
 
   // load j of this wave: rows (j * W + wave) * 8 + lane / 8 of the stage, weights first; chunk kc of the row
   const int lr = lane >> 3, kc16 = 16 * blk_pos(lr, lane & 7);
@@ -678,6 +659,71 @@ __global__ __launch_bounds__(KS* WN* WM * 64, 2) void k_block_tile(BlockGemmArgs
   }
 }
 
+// Tile idx of gx x rows: bands of 4 column tiles, row tile by row tile, so that
+// tiles in flight on one XCD share operands both ways.
+struct At {
+  int tx, ty;
+};
+__device__ __forceinline__ At place(int idx, int gx, int rows) {
+  const int band = idx / (4 * rows), in = idx - band * 4 * rows, wide = min(4, gx - 4 * band), ty = in / wide;
+  return {4 * band + in - ty * wide, ty};
+}
+
+// Tiles B in whole rounds of the chip, one to a CU; the rest of them, where that
+// is at most half a round, in tiles S, which take less time (S = B: none).
+// 4352 x 4096 x 4096, 272 tiles of 256 x 256: 77 us, 92 with the last 16 whole;
+// 8192 rows of 8 experts, 4096 x 4096: 155 against 169; 2000 rows of 64 experts,
+// 1536 x 2048 (256 x 128): 42.9 against 44.8.  128 x 128 tiles gain as much from
+// a split, but never so that they beat the other forms.
+constexpr int kRound = 256, kMostRest = kRound / 2;
+template <class B, class S>
+__device__ __host__ inline int rest_of_round(int tiles) {
+  const int rest = tiles % kRound;
+  return std::is_same<B, S>::value || tiles < kRound || rest > kMostRest ? 0 : rest;
+}
+
+// Experts: the tiles there are, not the bound that the grid is for, so that the
+// XCDs share them out evenly (5604 rows of 16 experts, 3424 x 3072: 111 us by
+// the bound).
+template <class B, class S, bool TAIL>
+__global__ __launch_bounds__(B::THREADS, 2) void k_block_tile(BlockGemmArgs a, int gx, int gy) {
+  static_assert(B::THREADS == S::THREADS, "one launch");
+  constexpr int PX = B::BN / S::BN, PARTS = PX * (B::BM / S::BM);
+  const int b = blockIdx.x;
+  At p;
+  int part = -1;  // of a split tile
+  auto mine = [&](int rows) {
+    const int rest = rest_of_round<B, S>(gx * rows), whole = gx * rows - rest;
+    if (b >= whole + PARTS * rest) return false;
+    if (b < whole) {
+      p = place(xcd_order(b, whole), gx, rows);
+    } else {
+      const int i = xcd_order(b - whole, PARTS * rest);
+      p = place(whole + i / PARTS, gx, rows);
+      part = i % PARTS;
+    }
+    return true;
+  };
+  RowTile t;
+  if (a.offsets) {
+    const RowTiles all(a.offsets, a.E, a.T, B::BM);
+    if (!mine(all.total)) return;
+    t = all.find(p.ty);
+  } else {
+    mine(gy);  // (the grid is exact)
+    t = {0, p.ty * B::BM, a.M};
+  }
+  if constexpr (PARTS > 1) {
+    if (part >= 0) {
+      t.t0 += S::BM * (part / PX);
+      const int n0 = p.tx * B::BN + S::BN * (part % PX);
+      if (t.t0 < t.end && n0 < a.N) tile<S, TAIL>(a, t, n0);
+      return;
+    }
+  }
+  tile<B, TAIL>(a, t, p.tx * B::BN);
+}
+
 }  // namespace
 
 // Row tiles of bm rows; for experts a bound on their number: every expert that has rows may end in a partial tile.
@@ -689,19 +735,20 @@ static int64_t row_tiles(const BlockGemmArgs& a, int64_t bm) {
 // A launch holds fewer than 2^32 threads (and its workgroups are numbered by ints).
 static bool too_many(int64_t groups, int threads) { return groups >= ((int64_t)1 << 32) / threads || groups >= INT32_MAX; }
 
-template <int BN, int BM, int WN, int WM, int NS, int KS>
+template <class B, class S>
 static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
-  using T = TileT<BN, BM, WN, WM, NS, KS>;
-  static_assert(T::SMEM <= 160 * 1024, "LDS of a CU");
-  constexpr int threads = KS * WN * WM * 64;
-  const int64_t gx = (a.N + BN - 1) / BN, gy = row_tiles(a, BM);
-  if (too_many(gx * gy, threads)) return hipErrorInvalidConfiguration;
+  constexpr int smem = B::SMEM > S::SMEM ? B::SMEM : S::SMEM, parts = B::BN * B::BM / (S::BN * S::BM);
+  static_assert(smem <= 160 * 1024, "LDS of a CU");
+  const int64_t gx = (a.N + B::BN - 1) / B::BN, gy = row_tiles(a, B::BM);
+  if (too_many(gx * gy + parts * kMostRest, B::THREADS)) return hipErrorInvalidConfiguration;
+  // (of experts the kernel counts the tiles)
+  const int64_t rest = a.offsets ? (parts > 1 ? kMostRest : 0) : rest_of_round<B, S>((int)(gx * gy));
   static std::atomic<int> allowed[2];
   const bool tail = a.K % 128 != 0;
-  const auto kern = tail ? k_block_tile<BN, BM, WN, WM, NS, KS, true> : k_block_tile<BN, BM, WN, WM, NS, KS, false>;
-  hipError_t e = allow_smem(kern, T::SMEM, allowed[tail]);
+  const auto kern = tail ? k_block_tile<B, S, true> : k_block_tile<B, S, false>;
+  hipError_t e = allow_smem(kern, smem, allowed[tail]);
   if (e != hipSuccess) return e;
-  return launch(kern, dim3((unsigned)(gx * gy)), threads, T::SMEM, s, a, (int)gx, (int)gy);
+  return launch(kern, dim3((unsigned)(gx * gy + (parts - 1) * rest)), B::THREADS, smem, s, a, (int)gx, (int)gy);
 }
 
 template <int NT, int MT, int W>
@@ -715,18 +762,27 @@ static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
 
 // Forms for many rows, widest first.  Time of a launch in us: 2.5 + rounds (start + blocks per_block), a round being
 // `at_once` tiles.  Fitted to N = 4096 with M of one full round at 32 scale blocks of K and M = 4096 at 4 (us: 63 and
-// 16.5, 36.5 and 18.3, 23.7 and 21.9, 14.9 and 37, 11.3 and 54, 16.6 and 28.5); other shapes came within 20 % of it.
+// 16.5, 36.5 and 18.3, 23.7 and 21.9, 14.9 and 37, 11.3 and 54, 16.6 and 28.5).  Rounds that are not full take up to
+// a third less; over 52 random shapes the form with the least time by it took 1.5 % more than the best one on average,
+// 23 % at worst.
 struct Form {
   int bn, bm, at_once;
   float start, per_block;
+  bool split;  // the rest of a round in 128 x 128
   hipError_t (*launch)(const BlockGemmArgs&, hipStream_t);
 };
-static const Form kForms[] = {{256, 256, 256, 7.4f, 1.66f, tile_launch<256, 256, 2, 4, 2, 1>},
-                              {256, 128, 256, 3.6f, 0.96f, tile_launch<256, 128, 4, 2, 3, 1>},
-                              {128, 128, 256, 2.5f, 0.58f, tile_launch<128, 128, 2, 4, 4, 1>},
-                              {128, 64, 256, 3.1f, 0.29f, tile_launch<128, 64, 2, 2, 3, 2>},
-                              {64, 64, 256, 2.4f, 0.20f, tile_launch<64, 64, 2, 2, 4, 2>},
-                              {64, 64, 512, 1.7f, 0.39f, tile_launch<64, 64, 2, 2, 4, 1>}};
+using Tile256 = Tile<256, 256, 2, 4, 2, 1>;
+using Tile256x128 = Tile<256, 128, 4, 2, 3, 1>;
+using Tile128 = Tile<128, 128, 2, 4, 4, 1>;
+using Tile128x64 = Tile<128, 64, 2, 2, 3, 2>;
+using Tile64 = Tile<64, 64, 2, 2, 4, 2>;
+using Tile64One = Tile<64, 64, 2, 2, 4, 1>;
+static const Form kForms[] = {{256, 256, 256, 7.4f, 1.66f, true, tile_launch<Tile256, Tile128>},
+                              {256, 128, 256, 3.6f, 0.96f, true, tile_launch<Tile256x128, Tile128>},
+                              {128, 128, 256, 2.5f, 0.58f, false, tile_launch<Tile128, Tile128>},
+                              {128, 64, 256, 3.1f, 0.29f, false, tile_launch<Tile128x64, Tile128x64>},
+                              {64, 64, 256, 2.4f, 0.20f, false, tile_launch<Tile64, Tile64>},
+                              {64, 64, 512, 1.7f, 0.39f, false, tile_launch<Tile64One, Tile64One>}};
 
 // Which form.  Times in us, of graphs of back-to-back launches.
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
@@ -760,7 +816,11 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
     const float n = tiles(f.bn, f.bm), rounds = ceilf(n / (float)f.at_once);
     // (two tiles share a CU only when there are more than 256)
     const float per = f.at_once == 512 && n <= 256.f ? 0.25f : f.per_block;
-    const float t = fmaxf(2.5f + rounds * (f.start + blocks * per), memory);
+    float t = 2.5f + rounds * (f.start + blocks * per);
+    const float rest = n - kRound * (rounds - 1.f);
+    if (f.split && rounds > 1.f && rest <= (float)kMostRest)
+      t += ceilf(rest / kRound * (float)(f.bn * f.bm / (128 * 128))) * (2.5f + blocks * 0.58f) - (f.start + blocks * per);
+    t = fmaxf(t, memory);
     if (!best || t < 0.97f * least) best = &f, least = t;
   }
   // The stream of 32 x 32 tiles keeps the chip filled where those are too few: 142 x 1224 x 3120 6.2 against 11.0,
