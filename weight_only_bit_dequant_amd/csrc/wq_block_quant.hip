@@ -84,7 +84,7 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
 // Below -88.6 exp(-g) leaves fp32 and the result is -0 (its size is below
 // 3e-37); above 90 exp(-g) no longer counts.  A NaN stays one.
 // Two library calls (expf and division) took 45 instructions an element, more
-// than the memory's time (8192 x 8192: 75 us; its 335 MB at 5.7 TB/s: 59 us).
+// than the memory's time (8192 x 8192: 75 us; so 65.5).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float L = -1.4426950216293335f, Ll = -1.9259629911e-8f;  // -log2 e = L + Ll
   constexpr float far = -88.6f;
@@ -103,7 +103,10 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 
 // ---------------------------------------------------------------- activation rows, gated activation
 // One lane per 8 elements, one 16-lane row per scale block; the blocks of all
-// rows are numbered through, so short rows share a workgroup.
+// rows are numbered through, so short rows share a workgroup.  Bound by memory:
+// the gate over 8192 x 8192 moves its 338 MB in 65.5 us, 5.2 TB/s (a copy of
+// that size 4.8); non-temporal loads, 512 threads and two blocks to a lane were
+// no faster.  64 x 2048 takes 2.6 us, 1 above an empty launch: one trip.
 // The row of a block is blk / KB as a product: with 2^sh < KB <= 2^(sh + 1) and
 // magic = ceil(2^(32 + sh) / KB), exact for blk < 2^31 (KB = 1: magic = 0).
 template <bool GATE>
@@ -137,7 +140,10 @@ __global__ __launch_bounds__(256) void k_block_quant_rows(const uint16_t* __rest
 // A row belongs to WPR waves and stays in their registers from its one read to
 // its one write: lane l of wave w holds chunks w * 64 + l + 64 * WPR * j
 // (8 elements each) for j < CPT, so its 16-lane rows are scale blocks.  The
-// sum of squares crosses lanes by shuffles and waves through LDS.
+// sum of squares crosses lanes by shuffles and waves through LDS.  Bound by
+// memory: 16384 x 8192 moves 941 MB in 160 us, 5.9 TB/s (a copy 4.8; two passes
+// over a row would read 537 MB again); a row of 4096 takes 2.6 us, one trip and
+// one meeting of its waves above an empty launch (1.6 us).
 template <int WPR>
 constexpr int norm_rows() {  // rows per workgroup: four waves or one row
   return WPR >= 3 ? 1 : 4 / WPR;
