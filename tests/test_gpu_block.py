@@ -248,7 +248,7 @@ def test_linear_rest_of_a_round(M, N, K):
     check_product(y[rows], (hx[rows], hs[rows], hw, hv))
 
 
-@pytest.mark.parametrize("counts,N", [([1000, 0, 1300, 2000], 4000), ([40, 700, 0, 290], 8192)])
+@pytest.mark.parametrize("counts,N", [([1000, 0, 1300, 2000], 4000), ([40, 700, 0, 290], 8192), ([100] * 17, 4096)])
 def test_grouped_rest_of_a_round(counts, N):
     case(f"grouped rest {counts} {N}")
     check_grouped(counts, N, 400, 900, 3)

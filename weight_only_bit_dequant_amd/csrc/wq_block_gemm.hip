@@ -805,9 +805,9 @@ static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
 
 // Forms for many rows, widest first.  Time of a launch in us: 2.5 + rounds (start + blocks per_block), a round being
 // `at_once` tiles.  Fitted to N = 4096 with M of one full round at 32 scale blocks of K and M = 4096 at 4 (us: 63 and
-// 16.5, 36.5 and 18.3, 23.7 and 21.9, 14.9 and 37, 11.3 and 54, 16.6 and 28.5).  Rounds that are not full take up to
-// a third less; over 52 random shapes the form with the least time by it took 1.5 % more than the best one on average,
-// 23 % at worst.
+// 16.5, 36.5 and 18.3, 23.7 and 21.9, 14.9 and 37, 11.3 and 54, 16.6 and 28.5).  A last round that is not full takes
+// down to 85 % of that, the fewer its tiles, and split into 128 x 128 theirs and 2 us.  Over 276 random shapes,
+// plain and grouped, the form with the least time by this took 0.6 % more than the best one on average, 9 % at worst.
 struct Form {
   int bn, bm, at_once;
   float start, per_block;
@@ -853,24 +853,25 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
     const float m = a.offsets ? (float)rows / (float)bm + 0.5f : (float)((rows + bm - 1) / bm);
     return (float)((a.N + bn - 1) / bn) * (float)groups * (m > 1.f ? m : 1.f);
   };
+  // Experts' tiles look for their rows first: 1 us a round, 2 in the stream's many workgroups.
+  const float look = a.offsets ? 1.0f : 0.0f;
   const Form* best = nullptr;
   float least = 0.f;
   for (const Form& f : kForms) {
-    const float n = tiles(f.bn, f.bm), rounds = ceilf(n / (float)f.at_once);
+    const float n = tiles(f.bn, f.bm), whole = ceilf(n / (float)f.at_once) - 1.f, rest = n - whole * (float)f.at_once;
     // (two tiles share a CU only when there are more than 256)
-    const float per = f.at_once == 512 && n <= 256.f ? 0.25f : f.per_block;
-    float t = 2.5f + rounds * (f.start + blocks * per);
-    const float rest = n - kRound * (rounds - 1.f);
-    if (f.split && rounds > 1.f && rest <= (float)kMostRest)
-      t += ceilf(rest / kRound * (float)(f.bn * f.bm / (128 * 128))) * (2.5f + blocks * 0.58f) - (f.start + blocks * per);
-    t = fmaxf(t, memory);
+    const float per = f.at_once == 512 && n <= 256.f ? 0.25f : f.per_block, round = f.start + look + blocks * per;
+    float last = round * (0.85f + 0.15f * rest / (float)f.at_once);
+    if (f.split && whole > 0.f && rest <= (float)kMostRest)
+      last = 2.f + ceilf(rest / kRound * (float)(f.bn * f.bm / (128 * 128))) * (2.5f + look + blocks * 0.58f);
+    const float t = fmaxf(2.5f + whole * round + last, memory);
     if (!best || t < 0.97f * least) best = &f, least = t;
   }
   // The stream of 32 x 32 tiles keeps the chip filled where those are too few: 142 x 1224 x 3120 6.2 against 11.0,
   // 94 x 2795 x 6144 11.1 against 14.8, 128 x 4096 x 4096 9.8 against 10.6; 256 x 4096 x 4096 16.7 against 11.3,
   // 697 x 1512 x 640 8.5 against 6.6.
   const float n = tiles(32, 32);
-  const float t = fmaxf(3.0f + 0.0045f * fmaxf(0.f, n - 300.f) + blocks * (0.09f + 0.00022f * n), memory);
+  const float t = fmaxf(3.0f + 2.f * look + 0.0045f * fmaxf(0.f, n - 300.f) + blocks * (0.09f + 0.00022f * n), memory);
   if (t < 0.97f * least) return stream_launch<2, 2, 4>(a, s);
   return best->launch(a, s);
 }
