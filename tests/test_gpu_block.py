@@ -248,6 +248,14 @@ def test_linear_rest_of_a_round(M, N, K):
     check_product(y[rows], (hx[rows], hs[rows], hw, hv))
 
 
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 2], 1000, 2064), ([17, 0, 5, 1] * 5, 392, 528),
+                                        ([16, 0, 40, 3, 1] * 26, 648, 272)])
+def test_grouped_few_rows(counts, N, K):
+    """16, 32 and 64 columns to a workgroup, by the number of tiles."""
+    case(f"grouped few rows {len(counts)} {N}x{K}")
+    check_grouped(counts, N, K, 70, 5, spare=3)
+
+
 @pytest.mark.parametrize("counts,N", [([1000, 0, 1300, 2000], 4000), ([40, 700, 0, 290], 8192), ([100] * 17, 4096)])
 def test_grouped_rest_of_a_round(counts, N):
     case(f"grouped rest {counts} {N}")

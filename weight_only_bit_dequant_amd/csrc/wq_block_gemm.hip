@@ -831,24 +831,35 @@ static const Form kForms[] = {{256, 256, 256, 7.4f, 1.66f, true, tile_launch<Til
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
   const int groups = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
   const int rows = (a.T + groups - 1) / groups;  // of an expert, on average (a.M for a plain Linear)
-  // Few rows: streamed.  Experts: 64 columns to a workgroup, so that fewer of them look for their rows (64 rows of
-  // 32 experts, 2048 x 2048: 17 against 24 with 16 columns and 22 with 256 x 128 tiles; 16 rows each: 26 against 39).
-  if (a.offsets && rows <= 16) return stream_launch<4, 1, 4>(a, s);
+  const int kb = (a.K + 127) / 128;
+  // Few rows: streamed.  Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best
+  // one to a workgroup, in eight waves where K is long enough for them; many share what they read and, of experts,
+  // look for their rows less often.
+  const int64_t cols = (a.N + 15) / 16;
+  if (a.offsets && rows <= 16) {
+    // (1 x 2 of 32, 1440 x 1920: 4.2 against 5.4 with 64 columns; 10 x 1 of 4, 3856 x 3184: 8.4 against 8.9 with 32 and
+    // 10.5 with 64; 6 x 2 of 16, 928 x 544: 4.2 with 32 against 4.6; 16 x 4 of 32, 2048 x 2048: 15.2 with 32, 16.6 with
+    // 64, 17.2 with 16; 128 x 4 of 64, 1536 x 2048: 29.0 with 64, 30.7 with 32, 44 with 16, 30 in 256 x 128 tiles)
+    const int64_t tiles = cols * groups;
+    if (tiles <= 256 || (tiles < 1024 && kb >= 16)) return stream_launch<1, 1, 8>(a, s);
+    if (tiles < 5120) return stream_launch<2, 1, 4>(a, s);
+    return stream_launch<4, 1, 4>(a, s);
+  }
   if (!a.offsets && rows <= 64) {
-    // Columns and rows to a workgroup by the number of 16 x 16 tiles: few keep the chip filled best one to a
-    // workgroup (1 x 4096 x 3072: 4.7 against 5.1 with two, 32 x 2048 x 2048: 3.6 against 4.2), many share what they
-    // read (32 x 4096 x 3072: 5.4 against 5.9; 32 x 8192 x 8192: 13.1 with four waves, 14.4 with eight, 16.2 with 16
-    // columns; 64 x 8192 x 8192: 16.3 with 32 x 32 against 17.5).
-    const int64_t tiles = ((a.N + 15) / 16) * (int64_t)((rows + 15) / 16);
-    if (tiles < 512) return stream_launch<1, 1, 8>(a, s);
-    if (tiles < 1024) return stream_launch<2, 1, 8>(a, s);
-    if (tiles == 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
+    // (1 x 4096 x 3072: 4.9 against 5.4 with 32 columns, 6.2 in four waves; 39 x 1592 x 3456: 4.8 with 32 in eight waves
+    // against 5.0 in four and 5.4 with 16; 4 x 7895 x 512: 3.75 with 32 in four waves against 4.0; 56 x 2672 x 1744 5.0
+    // against 5.9; 32 x 8192 x 8192: 13.1 with four waves, 14.4 with eight, 16.2 with 16 columns; 64 x 8192 x 8192:
+    // 16.5 with 32 x 32, 21.6 with 32 x 16)
+    const int64_t tiles = cols * ((rows + 15) / 16);
+    if (tiles <= 256) return stream_launch<1, 1, 8>(a, s);
+    if (tiles < 1024 && kb >= 16) return stream_launch<2, 1, 8>(a, s);
+    if (tiles <= 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<2, 2, 4>(a, s);
   }
   // More rows: the form with the least time, but no less than the memory's (weights, for experts those of all that
   // have rows), where the widest does best: fewer workgroups look for their rows (31 rows each of 64 experts, 1536 x
   // 2048: 45 with 256 x 128 tiles against 52-56 with the others).
-  const float blocks = (float)((a.K + 127) / 128), memory = 2.5f + (float)a.N * (float)a.K * (float)groups / 4.8e6f;
+  const float blocks = (float)kb, memory = 2.5f + (float)a.N * (float)a.K * (float)groups / 4.8e6f;
   auto tiles = [&](int bn, int bm) {  // an expert's last row tile is half full on average
     const float m = a.offsets ? (float)rows / (float)bm + 0.5f : (float)((rows + bm - 1) / bm);
     return (float)((a.N + bn - 1) / bn) * (float)groups * (m > 1.f ? m : 1.f);
