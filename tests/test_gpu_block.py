@@ -224,6 +224,12 @@ def test_linear(M, N, K):
     check_product(y, (host(xq), host(xs), host(q["codes"]), host(q["scales"])), bias)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 200, 5632), (3, 2500, 6160), (30, 1000, 7424), (64, 136, 16400)])
+def test_linear_long_and_narrow(M, N, K):
+    """Two blocks of a wave under way; runs of blocks that end in the middle of a wave's share."""
+    test_linear(M, N, K)
+
+
 @pytest.mark.parametrize("M,N,K", [(2048, 2304, 1280), (1900, 4000, 272), (4096, 2048, 2048), (3000, 2500, 1040)])
 def test_linear_large(M, N, K):
     """Whole outputs of the large-tile forms."""
@@ -248,7 +254,7 @@ def test_linear_rest_of_a_round(M, N, K):
     check_product(y[rows], (hx[rows], hs[rows], hw, hv))
 
 
-@pytest.mark.parametrize("counts,N,K", [([1, 0, 2], 1000, 2064), ([17, 0, 5, 1] * 5, 392, 528),
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 2], 1000, 2064), ([17, 0, 5, 1] * 5, 392, 528), ([1, 0, 2], 600, 5776),
                                         ([16, 0, 40, 3, 1] * 26, 648, 272)])
 def test_grouped_few_rows(counts, N, K):
     """16, 32 and 64 columns to a workgroup, by the number of tiles."""

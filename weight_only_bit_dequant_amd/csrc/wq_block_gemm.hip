@@ -136,19 +136,20 @@ __device__ __forceinline__ int blk_pos(int r, int k) { return k ^ (((r >> 1) & 1
 // x 3072 5.4-5.9 us either way; 64 rows of 32 experts, 2048 x 2048: 17 against
 // 15-17 us).  What bounds it is the weights' stream (those 64 rows: 118 MB in 17
 // us, 7 TB/s where the Infinity Cache holds some of them) and, below some 10 MB,
-// the trips to memory: 1 x 4096 x 3072 takes 4.7 us, 12.6 MB at 2.7 TB/s.
+// the trips to memory: 1 x 4096 x 3072 takes 4.7 us, 12.6 MB at 2.7 TB/s.  SL: slots
+// of a wave, blocks under way.
 constexpr int kRun = 8;  // blocks whose scales a wave holds at a time
 
-template <int NT, int MT, int W>
+template <int NT, int MT, int W, int SL>
 struct StreamT {
   static constexpr int SLOT = (NT + MT) * 2048, L = 2 * (NT + MT);  // bytes and loads per block
   static constexpr int PART = W * 16 * MT * 16 * NT * 4;
-  static constexpr int SMEM = W * SLOT > PART ? W * SLOT : PART;
+  static constexpr int SMEM = SL * W * SLOT > PART ? SL * W * SLOT : PART;
 };
 
-template <int NT, int MT, int W>
+template <int NT, int MT, int W, int SL>
 __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx, int gy) {
-  using S = StreamT<NT, MT, W>;
+  using S = StreamT<NT, MT, W, SL>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -205,8 +206,9 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
   for (int j = 0; j < MT; ++j) sa[j] = a.Xs + (int64_t)((uint32_t)src[j] < (uint32_t)a.M ? src[j] : 0) * KB;
   const float* sb = a.Ws + ((int64_t)t.e * NBLK + n0 / 128) * KB;  // 16 NT columns lie in one block
 
-  unsigned char* slot = smem + wave * S::SLOT;
-  auto issue = [&](int kt) {
+  unsigned char* slot0 = smem + wave * SL * S::SLOT;
+  auto issue = [&](int kt, int at) {
+    unsigned char* slot = slot0 + at * S::SLOT;
 #pragma unroll
     for (int l = 0; l < S::L; ++l)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(l < 2 * NT ? Wr : Xr,
@@ -214,8 +216,8 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
                                                (int)(kt * 128 + kc16 < K ? voff[l] : kOut), kt * 128, 0, 0);
   };
   const int flo = c * 128 + blk_pos(c, 2 * g) * 16;
-  auto frag = [&](int i) {
-    const unsigned char* p = slot + i * 2048;
+  auto frag = [&](int at, int i) {
+    const unsigned char* p = slot0 + at * S::SLOT + i * 2048;
     return join(*reinterpret_cast<const u32x4*>(p + flo), *reinterpret_cast<const u32x4*>(p + (flo ^ 16)));
   };
 
@@ -228,7 +230,6 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
   const int per = (KB + W - 1) / W, end = min(KB, (wave + 1) * per);
   for (int k0 = wave * per; k0 < end; k0 += kRun) {
     const int n = min(kRun, end - k0);
-    issue(k0);
     // scales of kRun blocks from `first` on, so that none is read past the row; block k0 + u is number u + back
     const int first = max(0, min(k0, KB - kRun)), back = k0 - first;
     const Scales<kRun> bv = load_scales<kRun>(sb + first, KB);
@@ -236,26 +237,37 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       av[j] = load_scales<kRun>(sa[j] + first, KB);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < SL; ++u)
+      if (u < n) issue(k0 + u, u);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int u = 0; u < kRun; ++u) av[j].v[u] = (uint32_t)src[j] < (uint32_t)a.M ? av[j].v[u] * bv.v[u] : 0.f;
-    }
 #pragma unroll
     for (int u = 0; u < kRun; ++u) {
       if (u < n) {
-        __builtin_amdgcn_s_waitcnt(kWaitVm0);
+        constexpr int NEWER = (SL - 1) * S::L;  // loads that may still be under way
+        if (SL > 1 && u + SL <= n)
+          __builtin_amdgcn_s_waitcnt(kWaitVm0 | (NEWER & 15) | ((NEWER >> 4) << 14));
+        else
+          __builtin_amdgcn_s_waitcnt(kWaitVm0);
         asm volatile("" ::: "memory");
         i32x8 B[MT];
         float sc[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          B[j] = frag(NT + j);
+          B[j] = frag(u % SL, NT + j);
           sc[j] = av[j].v[0];
 #pragma unroll
           for (int v = 1; v < kRun; ++v) sc[j] = u + back == v ? av[j].v[v] : sc[j];
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const i32x8 A = frag(i);
+          const i32x8 A = frag(u % SL, i);
 #pragma unroll
           for (int j = 0; j < MT; ++j) {
             const f32x4 p = mfma_blk(A, B[j]);
@@ -265,7 +277,7 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
         }
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);  // the slot has been read
         asm volatile("" ::: "memory");
-        if (u + 1 < n) issue(k0 + u + 1);
+        if (u + SL < n) issue(k0 + u + SL, u % SL);
       }
     }
   }
@@ -794,13 +806,13 @@ static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   return launch(kern, dim3((unsigned)(gx * gy + (parts - 1) * rest)), B::THREADS, smem, s, a, (int)gx, (int)gy);
 }
 
-template <int NT, int MT, int W>
+template <int NT, int MT, int W, int SL = 1>
 static hipError_t stream_launch(const BlockGemmArgs& a, hipStream_t s) {
-  constexpr int smem = StreamT<NT, MT, W>::SMEM;
+  constexpr int smem = StreamT<NT, MT, W, SL>::SMEM;
   static_assert(smem <= 65536, "no leave needed for the LDS size");
   const int64_t gx = (a.N + 16 * NT - 1) / (16 * NT), gy = row_tiles(a, 16 * MT);
   if (too_many(gx * gy, W * 64)) return hipErrorInvalidConfiguration;
-  return launch(k_block_stream<NT, MT, W>, dim3((unsigned)(gx * gy)), W * 64, smem, s, a, (int)gx, (int)gy);
+  return launch(k_block_stream<NT, MT, W, SL>, dim3((unsigned)(gx * gy)), W * 64, smem, s, a, (int)gx, (int)gy);
 }
 
 // Forms for many rows, widest first.  Time of a launch in us: 2.5 + rounds (start + blocks per_block), a round being
@@ -836,11 +848,16 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
   // one to a workgroup, in eight waves where K is long enough for them; many share what they read and, of experts,
   // look for their rows less often.
   const int64_t cols = (a.N + 15) / 16;
+  // Long and narrow: a wave's trips to memory one after the other are the time, so two of its blocks are under way
+  // (4 x 2344 x 7552: 6.05 against 7.0, 16 x 1024 x 16384 9.3 against 10.8, 32 x 2048 x 5632 5.6 against 6.1; not
+  // where the stream itself is: 1 x 4096 x 8192 7.8 against 7.6, 1 x 512 x 8192 5.1 against 5.0).
+  const bool deep = kb >= 44 && a.N <= 2560;
   if (a.offsets && rows <= 16) {
     // (1 x 2 of 32, 1440 x 1920: 4.2 against 5.4 with 64 columns; 10 x 1 of 4, 3856 x 3184: 8.4 against 8.9 with 32 and
     // 10.5 with 64; 6 x 2 of 16, 928 x 544: 4.2 with 32 against 4.6; 16 x 4 of 32, 2048 x 2048: 15.2 with 32, 16.6 with
     // 64, 17.2 with 16; 128 x 4 of 64, 1536 x 2048: 29.0 with 64, 30.7 with 32, 44 with 16, 30 in 256 x 128 tiles)
     const int64_t tiles = cols * groups;
+    if (tiles <= 256 && deep) return stream_launch<1, 1, 8, 2>(a, s);
     if (tiles <= 256 || (tiles < 1024 && kb >= 16)) return stream_launch<1, 1, 8>(a, s);
     if (tiles < 5120) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<4, 1, 4>(a, s);
@@ -851,7 +868,7 @@ hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
     // against 5.9; 32 x 8192 x 8192: 13.1 with four waves, 14.4 with eight, 16.2 with 16 columns; 64 x 8192 x 8192:
     // 16.5 with 32 x 32, 21.6 with 32 x 16)
     const int64_t tiles = cols * ((rows + 15) / 16);
-    if (tiles <= 256) return stream_launch<1, 1, 8>(a, s);
+    if (tiles <= 256) return deep ? stream_launch<1, 1, 8, 2>(a, s) : stream_launch<1, 1, 8>(a, s);
     if (tiles < 1024 && kb >= 16) return stream_launch<2, 1, 8>(a, s);
     if (tiles <= 1024 || rows <= 16) return stream_launch<2, 1, 4>(a, s);
     return stream_launch<2, 2, 4>(a, s);
