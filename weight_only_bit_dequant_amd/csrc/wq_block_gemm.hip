@@ -131,13 +131,12 @@ __device__ __forceinline__ int blk_pos(int r, int k) { return k ^ (((r >> 1) & 1
 // its own in LDS (buffer_load ... lds, 8 whole 128-byte rows per instruction)
 // and reads them back as operands: loaded as operands, 16 rows of 64 bytes per
 // instruction, rows a power of two apart took twice as long (16 x 512 x 8192:
-// 11.3 against 4.9 us).  Waves meet once, to add up their sums.  One slot per
-// wave and more workgroups on a CU did as well as two or three slots (32 x 4096
-// x 3072 5.4-5.9 us either way; 64 rows of 32 experts, 2048 x 2048: 17 against
-// 15-17 us).  What bounds it is the weights' stream (those 64 rows: 118 MB in 17
-// us, 7 TB/s where the Infinity Cache holds some of them) and, below some 10 MB,
-// the trips to memory: 1 x 4096 x 3072 takes 4.7 us, 12.6 MB at 2.7 TB/s.  SL: slots
-// of a wave, blocks under way.
+// 11.3 against 4.9 us).  Waves meet once, to add up their sums.  A wave has SL
+// slots, blocks under way: one, and more workgroups on a CU, does as well as two
+// or three (32 x 4096 x 3072 5.5 us either way) but where few workgroups have long
+// runs.  What bounds it is the weights' stream (64 rows of 32 experts, 2048 x 2048:
+// 118 MB in 15.2 us, some of them from the Infinity Cache) and, below some 10 MB,
+// the trips to memory: 1 x 4096 x 3072 takes 4.7 us, 12.6 MB at 2.7 TB/s.
 constexpr int kRun = 8;  // blocks whose scales a wave holds at a time
 
 template <int NT, int MT, int W, int SL>
