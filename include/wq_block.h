@@ -74,8 +74,9 @@ wq_status wq_block_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* 
  * Gated activation with a quantized result: GU holds rows of 2 K bf16 values
  * (row m at GU + m * ldg elements; ldg >= 2 K, ldg % 8 == 0), gate first;
  *   y[k] = silu(GU[m][k]) * GU[m][K + k],  silu(g) = g / (1 + exp(-g))
- * in fp32 (-0 for g < -88.6, where exp(-g) leaves fp32's range).  Xq/Xs receive
- * y quantized.
+ * in fp32 (silu is -0 for finite g < -88.6, where exp(-g) leaves fp32's range,
+ * g for infinite g > 0 and NaN for g = -infinity, as the formula has them).
+ * Xq/Xs receive y quantized.
  */
 wq_status wq_block_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int64_t K, void* Xq, float* Xs,
                                      void* stream);

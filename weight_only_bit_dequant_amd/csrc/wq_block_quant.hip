@@ -82,7 +82,10 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
 //   reciprocal of d' (1 ulp).  d' = 2^-8 (1 + exp(-g)) and g' = 2^-8 g: r stays a
 //   normal number up to the largest d (reciprocals below 2^-126 read as 0).
 // Below -88.6 exp(-g) leaves fp32 and the result is -0 (its size is below
-// 3e-37); above 90 exp(-g) no longer counts.  A NaN stays one.
+// 3e-37); above 90 exp(-g) no longer counts and the result is g.  Both are g
+// times 0 or 1, so that +infinity stays one and -infinity (an infinity over an
+// infinity) and NaN give NaN: the quotient's correction would make NaN of both
+// infinities.
 // Two library calls (expf and division) took 45 instructions an element, more
 // than the memory's time (8192 x 8192: 75 us; so 65.5).
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -98,7 +101,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   const float q = n * r;
   float v = __builtin_fmaf(__builtin_fmaf(-q, d, n), r, q);
   asm("" : "+v"(v));  // a select, not a branch around the quotient for each element
-  return (g < far ? -0.0f : v) * u;
+  return (x == g ? v : g * (g > 0.0f ? 1.0f : 0.0f)) * u;
 }
 
 // ---------------------------------------------------------------- activation rows, gated activation
