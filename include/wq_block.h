@@ -14,8 +14,10 @@
  *          within one ulp of IEEE division's, and by the choice of s at most 448.
  *          The floor 2^-126 keeps 1 / s finite: an all-zero block has that scale
  *          and codes 0.
- * A block that holds a NaN has the scale NaN, one that holds an infinity (and no
- * NaN) the scale infinity: no finite value is made up for it.
+ * A block that holds a NaN has the scale NaN and codes NaN, one that holds an
+ * infinity (and no NaN) the scale infinity, codes NaN for its infinities and
+ * zeros of their sign for its finite values: code * scale is NaN throughout, and
+ * no finite value is made up for it.
  *
  * Conventions are those of wq.h: device pointers owned by the caller, row-major
  * tensors, bf16 as uint16 bit patterns, stream-ordered calls that neither wait

@@ -63,14 +63,15 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
 // remainder: IEEE division's result but for rare last bits, at a third of its
 // instructions.  (y * (1 / s) alone rounds four times as many codes to the
 // other neighbour as the fp32 definition does.)  |y / s| <= 448 by the choice
-// of s, so nothing is clamped.
+// of s, so nothing is clamped.  Over an infinite s the quotient is y * 0 already
+// (a zero, NaN for an infinite y): its remainder, 0 * s off, would be NaN for all.
 __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
-  const float inv = 1.0f / s;
+  const float inv = 1.0f / s, back = s < __builtin_inff() ? s : 0.0f;
   F8 q;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float v = y.v[i] * inv;
-    q.v[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-v, s, y.v[i]), inv, v), v);  // (-0 would become 0)
+    q.v[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-v, back, y.v[i]), inv, v), v);  // (-0 would become 0)
   }
   return u32x2{e4m3_pack4(q.v[0], q.v[1], q.v[2], q.v[3]), e4m3_pack4(q.v[4], q.v[5], q.v[6], q.v[7])};
 }
