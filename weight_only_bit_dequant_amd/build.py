@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libwq.so")
 EXT = os.path.join(HERE, "_block_call.so")
 
 SOURCES = ["wq_api.hip", "wq_plan.cpp", "wq_quant.hip", "wq_linear.hip", "wq_gemm_tiled.hip", "wq_gemm_mid.hip", "wq_mx.hip", "wq_mlp.hip", "wq_noalloc.hip",
-           "wq_block_api.hip", "wq_block_quant.hip", "wq_block_gemm.hip"]
+           "wq_block_api.hip", "wq_block_plan.cpp", "wq_block_quant.hip", "wq_block_gemm.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

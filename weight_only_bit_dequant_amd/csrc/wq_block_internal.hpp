@@ -64,4 +64,20 @@ struct BlockGemmArgs {
 };
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s);
 
+// A round of the chip in tiles, and the largest rest of one that is split into smaller ones (wq_block_gemm.hip).
+constexpr int kRound = 256, kMostRest = kRound / 2;
+
+// Kernel forms of the products, by columns x rows of a workgroup: streams of the weights for few rows (deep: two
+// blocks of a wave under way; eight: waves, where the others of 32 columns have four), LDS tiles for more (one:
+// 64 x 64 without K split).
+enum BlockForm {
+  kStream16, kStream16Deep, kStream32Eight, kStream32, kStream32x32, kStream64,
+  kTile256, kTile256x128, kTile128, kTile128x64, kTile64, kTile64One, kBlockForms
+};
+// The form of T rows of Y over E experts (a plain Linear: grouped false), chosen on the host (wq_block_plan.cpp).
+BlockForm block_form(bool grouped, int T, int E, int N, int K);
+
 }  // namespace wq
+
+// The form's name, for tests (E = 0: a plain Linear).
+extern "C" const char* wq_block_form(int64_t T, int64_t E, int64_t N, int64_t K);
