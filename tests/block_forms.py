@@ -57,3 +57,28 @@ def form(T, N, K, E=0):
     f = wq.lib().wq_block_form
     f.restype, f.argtypes = ctypes.c_char_p, [ctypes.c_int64] * 4
     return f(T, E, N, K).decode()
+
+
+ROUND, MOST_REST = 256, 128  # tiles in a round of the chip; the largest rest of one that is split
+_SPLIT_TILES = {"tile 256x256": (256, 256), "tile 256x128": (256, 128)}
+
+
+def rest(form, counts, N):
+    """Tiles of the last round that are computed in 128 x 128 pieces, for the rows of each expert ([M]: plain)."""
+    if form not in _SPLIT_TILES:
+        return 0
+    bn, bm = _SPLIT_TILES[form]
+    tiles = -(-N // bn) * sum(-(-c // bm) for c in counts)
+    return tiles % ROUND if tiles >= ROUND and tiles % ROUND <= MOST_REST else 0
+
+
+# As PLAIN and GROUPED, with a last round that is split.
+PLAIN_SPLIT = [
+    ("tile 256x128", 2573, 7577, 2176), ("tile 256x128", 2833, 6734, 2208), ("tile 256x128", 3387, 5699, 16),
+    ("tile 256x256", 2362, 6940, 2176), ("tile 256x256", 2317, 6696, 2096), ("tile 256x256", 4300, 4096, 528),
+]
+GROUPED_SPLIT = [
+    ("tile 256x128", [260, 260, 293], 7190, 2096, 500, 0), ("tile 256x128", [270, 260, 300], 7184, 2176, None, 0),
+    ("tile 256x128", _uneven(70, 1240), 1111, 2288, None, 0), ("tile 256x128", _uneven(70, 1192), 1144, 2048, 700, 0),
+    ("tile 256x256", [520, 522, 600], 7642, 2096, None, 0), ("tile 256x256", [600, 518, 514], 7184, 2176, 900, 0),
+]

@@ -41,6 +41,19 @@ def test_every_form_has_sizes():
     assert {f for f, c, *_ in F.GROUPED if len(c) > 64 and f.startswith("tile")} == {n for n in names if n.startswith("tile")}
 
 
+def test_sizes_that_split_a_round():
+    text = open(os.path.join(ROOT, "weight_only_bit_dequant_amd", "csrc", "wq_block_internal.hpp")).read()
+    assert "kRound = %d, kMostRest = kRound / %d" % (F.ROUND, F.ROUND // F.MOST_REST) in text
+    for form, M, N, K in F.PLAIN_SPLIT:
+        assert F.form(M, N, K) == form and F.rest(form, [M], N) > 0, (form, M, N, K)
+    for form, counts, N, K, _, spare in F.GROUPED_SPLIT:
+        assert F.form(sum(counts) + spare, N, K, len(counts)) == form and F.rest(form, counts, N) > 0, (form, counts, N)
+    for sizes in (F.PLAIN_SPLIT, F.GROUPED_SPLIT):  # both forms that split, with and without a short last block
+        assert {(s[0], s[3] % 128 == 0) for s in sizes} == {(f, w) for f in F._SPLIT_TILES for w in (True, False)}
+    # and the others leave their tiles whole
+    assert not any(F.rest(f, [M], N) for f, M, N, _ in F.PLAIN) and not any(F.rest(s[0], s[1], s[2]) for s in F.GROUPED)
+
+
 @pytest.mark.parametrize("T,E,N,K", [(1, 0, 4096, 3072), (32, 0, 4096, 3072), (300, 0, 6152, 4096), (8192, 0, 8192, 8192),
                                      (64, 32, 2048, 2048), (2000, 64, 1536, 2048), (8192, 8, 4096, 4096)])
 def test_measured_sizes_take_a_tested_kernel(T, E, N, K):

@@ -37,6 +37,21 @@ def test_grouped_form(form, counts, N, K, M, spare):
     check_grouped(counts, N, K, M, 31, spare=spare)
 
 
+@pytest.mark.parametrize("form,M,N,K", F.PLAIN_SPLIT)
+def test_linear_split_round(form, M, N, K):
+    """A few tiles more than whole rounds of the chip: those in 128 x 128 pieces, every output compared."""
+    case(f"linear split {form}: {M}x{N}x{K}")
+    assert F.form(M, N, K) == form and F.rest(form, [M], N) > 0
+    check_linear(M, N, K)
+
+
+@pytest.mark.parametrize("form,counts,N,K,M,spare", F.GROUPED_SPLIT)
+def test_grouped_split_round(form, counts, N, K, M, spare):
+    case(f"grouped split {form}: {sum(counts)} of {len(counts)} {N}x{K}")
+    assert F.form(sum(counts) + spare, N, K, len(counts)) == form and F.rest(form, counts, N) > 0
+    check_grouped(counts, N, K, M, 32, spare=spare)
+
+
 def test_tiled_weights_past_32_bit_offsets():
     """The last of nine experts' weights start at byte 2^32; its rows go through a tiled form."""
     E, N, K, T = 9, 16384, 32768, 160
