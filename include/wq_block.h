@@ -105,7 +105,9 @@ wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K,
  *   Wq, Ws  : weights of the E experts
  *   Y       : bf16 [T][N]
  * Nothing is read back to the host: T and E alone decide the launch.  Entries
- * of offsets are clamped to [0, T], so no value of them reaches outside Y.
+ * of offsets are clamped to [0, T] and the tiles they make to those launched, so
+ * no value of them reaches outside Y or the operands (out of order, which rows
+ * are written by which expert is not defined).
  * M * K < 2^32 with rows (WQ_EUNSUPPORTED otherwise).
  */
 wq_status wq_block_grouped_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const int32_t* rows,

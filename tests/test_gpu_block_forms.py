@@ -69,3 +69,16 @@ def test_tiled_weights_past_32_bit_offsets():
         at = slice(n, n + 128)
         check_product(C.bf16_to_f32(host(y[:, at].contiguous())).astype(np.float64),
                       (host(xq), host(xs), host(codes[E - 1, at]), host(scales[E - 1, n // 128 : n // 128 + 1])))
+
+
+@pytest.mark.parametrize("T,E,N,K", [(40, 64, 136, 272), (300, 9, 1040, 400), (2000, 40, 1000, 144)])
+def test_offsets_out_of_order_stay_inside(T, E, N, K):
+    """Decreasing offsets count more tiles than are launched: the rows after Y's stay as they were."""
+    case(f"grouped offsets out of order {T} {E} {N}x{K} {F.form(T, N, K, E)}")
+    xq, xs = block.quantize_act(up(rows_bits(T, K, 1)))
+    q = weight(N, K, 2, E)
+    off = torch.tensor([0 if e % 2 == 0 else T for e in range(E + 1)], dtype=torch.int32, device=DEV)
+    buf = torch.full((T + 300, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = block.grouped_linear(xq, xs, q, off, out=buf[:T])
+    assert y.data_ptr() == buf.data_ptr()
+    assert bool((buf[T:] == 7.0).all()) and bool(torch.isfinite(y.float()).all())

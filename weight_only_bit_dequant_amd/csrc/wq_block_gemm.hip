@@ -6,9 +6,7 @@
 // and adds to the fp32 sum (one fused multiply-add per output and block).  The
 // weights are operand A, so a lane's four results are four columns n of one
 // row m: one activation scale, one weight scale, 8 bytes of bf16 output.
-#include <type_traits>
-
-#include "wq_block_internal.hpp"
+#include "wq_block_tiles.hpp"
 #include "wq_kernel_common.hpp"
 
 namespace wq {
@@ -50,13 +48,6 @@ __device__ __forceinline__ Scales<CH> load_scales(const float* p, int KB) {
     for (int i = 0; i < CH; ++i) s.v[i] = p[min(i, KB - 1)];
   }
   return s;
-}
-
-// Place of workgroup b of G in an order that the XCDs share out in contiguous
-// pieces (workgroup b runs on XCD b % 8, and each XCD has its own L2).
-__device__ __forceinline__ int xcd_order(int b, int G) {
-  const int q = G >> 3, r = G & 7, x = b & 7;
-  return x * q + min(x, r) + (b >> 3);
 }
 
 // Inclusive sum over the lanes: shifts within rows of 16, then each row's last
@@ -152,21 +143,17 @@ __global__ __launch_bounds__(W * 64) void k_block_stream(BlockGemmArgs a, int gx
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = a.N, K = a.K, KB = (K + 127) >> 7, NBLK = (N + 127) >> 7;
-  // consecutive workgroups of an XCD take the row tiles of one column tile, which share its weights
   RowTile t;
-  int tx;
+  At p;
   if (a.offsets) {
     const RowTiles all(a.offsets, a.E, a.T, 16 * MT);
-    if ((int)blockIdx.x >= gx * all.total) return;  // the grid is for a bound on their number
-    const int tile = xcd_order(blockIdx.x, gx * all.total);
-    tx = tile / all.total;
-    t = all.find(tile - tx * all.total);
+    if (!stream_at(blockIdx.x, gx, all.total, gy, p)) return;  // the grid is for a bound on their number
+    t = all.find(p.ty);
   } else {
-    const int tile = xcd_order(blockIdx.x, gx * gy), ty = tile % gy;
-    tx = tile / gy;
-    t = {0, ty * 16 * MT, a.M};
+    stream_at(blockIdx.x, gx, gy, gy, p);
+    t = {0, p.ty * 16 * MT, a.M};
   }
-  const int n0 = tx * 16 * NT;
+  const int n0 = p.tx * 16 * NT;
 
   const __amdgpu_buffer_rsrc_t Wr =
       make_rsrc(a.Wq + ((int64_t)t.e * N + n0) * K, (uint32_t)min(16 * NT, N - n0) * (uint32_t)K);
@@ -712,28 +699,13 @@ __device__ __forceinline__ void tile(const BlockGemmArgs& a, const RowTile t, co
   }
 }
 
-// Tile idx of gx x rows: bands of 4 column tiles, row tile by row tile, so that
-// tiles in flight on one XCD share operands both ways.
-struct At {
-  int tx, ty;
-};
-__device__ __forceinline__ At place(int idx, int gx, int rows) {
-  const int band = idx / (4 * rows), in = idx - band * 4 * rows, wide = min(4, gx - 4 * band), ty = in / wide;
-  return {4 * band + in - ty * wide, ty};
-}
-
 // Tiles B in whole rounds of the chip, one to a CU; the rest of them, where that
 // is at most half a round, in tiles S, which take less time (S = B: none).
 // 4352 x 4096 x 4096, 272 tiles of 256 x 256: 77 us, 92 with the last 16 whole;
 // 8192 rows of 8 experts, 4096 x 4096: 155 against 169; 2000 rows of 64 experts,
 // 1536 x 2048 (256 x 128): 42.9 against 44.8.  128 x 128 tiles gain as much from
 // a split, but never so that they beat the other forms.
-template <class B, class S>
-__device__ __host__ inline int rest_of_round(int tiles) {
-  const int rest = tiles % kRound;
-  return std::is_same<B, S>::value || tiles < kRound || rest > kMostRest ? 0 : rest;
-}
-
+//
 // Experts: the tiles there are, not the bound that the grid is for, so that the
 // XCDs share them out evenly (5604 rows of 16 experts, 3424 x 3072: 111 us by
 // the bound).
@@ -743,26 +715,14 @@ __global__ __launch_bounds__(B::THREADS, 2) void k_block_tile(BlockGemmArgs a, i
   constexpr int PX = B::BN / S::BN, PARTS = PX * (B::BM / S::BM);
   const int b = blockIdx.x;
   At p;
-  int part = -1;  // of a split tile
-  auto mine = [&](int rows) {
-    const int rest = rest_of_round<B, S>(gx * rows), whole = gx * rows - rest;
-    if (b >= whole + PARTS * rest) return false;
-    if (b < whole) {
-      p = place(xcd_order(b, whole), gx, rows);
-    } else {
-      const int i = xcd_order(b - whole, PARTS * rest);
-      p = place(whole + i / PARTS, gx, rows);
-      part = i % PARTS;
-    }
-    return true;
-  };
+  int part;
   RowTile t;
   if (a.offsets) {
     const RowTiles all(a.offsets, a.E, a.T, B::BM);
-    if (!mine(all.total)) return;
+    if (!tile_at(b, gx, all.total, gy, PARTS, p, part)) return;
     t = all.find(p.ty);
   } else {
-    mine(gy);  // (the grid is exact)
+    tile_at(b, gx, gy, gy, PARTS, p, part);  // (the grid is exact)
     t = {0, p.ty * B::BM, a.M};
   }
   if constexpr (PARTS > 1) {
@@ -794,7 +754,7 @@ static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   const int64_t gx = (a.N + B::BN - 1) / B::BN, gy = row_tiles(a, B::BM);
   if (too_many(gx * gy + parts * kMostRest, B::THREADS)) return hipErrorInvalidConfiguration;
   // (of experts the kernel counts the tiles)
-  const int64_t rest = a.offsets ? (parts > 1 ? kMostRest : 0) : rest_of_round<B, S>((int)(gx * gy));
+  const int64_t rest = a.offsets ? (parts > 1 ? kMostRest : 0) : rest_of_round(parts > 1, (int)(gx * gy));
   static std::atomic<int> allowed[2];
   const bool tail = a.K % 128 != 0;
   const auto kern = tail ? k_block_tile<B, S, true> : k_block_tile<B, S, false>;

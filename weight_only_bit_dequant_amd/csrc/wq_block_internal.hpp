@@ -64,7 +64,7 @@ struct BlockGemmArgs {
 };
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s);
 
-// A round of the chip in tiles, and the largest rest of one that is split into smaller ones (wq_block_gemm.hip).
+// A round of the chip in tiles, and the largest rest of one that is split into smaller ones (wq_block_tiles.hpp).
 constexpr int kRound = 256, kMostRest = kRound / 2;
 
 // Kernel forms of the products, by columns x rows of a workgroup: streams of the weights for few rows (deep: two
