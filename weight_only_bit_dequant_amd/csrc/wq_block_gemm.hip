@@ -755,7 +755,7 @@ static hipError_t tile_launch(const BlockGemmArgs& a, hipStream_t s) {
   if (too_many(gx * gy + parts * kMostRest, B::THREADS)) return hipErrorInvalidConfiguration;
   // (of experts the kernel counts the tiles)
   const int64_t rest = a.offsets ? (parts > 1 ? kMostRest : 0) : rest_of_round(parts > 1, (int)(gx * gy));
-  static std::atomic<int> allowed[2];
+  static SmemAllowed allowed[2];
   const bool tail = a.K % 128 != 0;
   const auto kern = tail ? k_block_tile<B, S, true> : k_block_tile<B, S, false>;
   hipError_t e = allow_smem(kern, smem, allowed[tail]);

@@ -306,7 +306,7 @@ hipError_t launch_mid_nb(const LinearArgs& a, hipStream_t s) {
   constexpr int part = kMidWaves * kMidBM * kMidPW * 4;
   constexpr int sm = ring > part ? ring : part;
   static_assert(sm <= 160 * 1024, "exceeds the LDS of a CU");
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_gemm_mid<F, WL, NBMAX>;
   hipError_t e = allow_smem(k, sm, done);
   if (e != hipSuccess) return e;

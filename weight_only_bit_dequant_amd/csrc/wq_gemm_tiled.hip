@@ -688,7 +688,7 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
   constexpr int sm = KS * tile_smem<F, BM, BN>();
   static_assert(sm <= 160 * 1024, "tile exceeds the LDS of a CU");
   static_assert(KS == 1 || (KS - 1) * BM * BN * 4 <= sm, "group partials must fit in the tile buffers");
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_gemm_tiled<F, BM, BN, tile_stages<BM, BN>(), KS, WGN, WL>;
   hipError_t e = allow_smem(k, sm, done);
   if (e != hipSuccess) return e;
@@ -707,7 +707,7 @@ hipError_t launch_tiled_f(const LinearArgs& a, const LinearPlan& p, hipStream_t 
   // them (no K groups); the other shapes run with one or two K groups
   if constexpr (F == KF_MXFP4) {
     if (p.bm == 256) {
-      static std::atomic<int> done_dw{0}, done_b{0};
+      static SmemAllowed done_dw{0}, done_b{0};
       constexpr int sm = (2 * 256 * 256 > 8 * 128 * kTileRowBytes) ? 2 * 256 * 256 : 8 * 128 * kTileRowBytes;
       const bool dw = a.K % 128 == 0;
       auto k = dw ? k_mx_wreg<WL, true> : k_mx_wreg<WL, false>;
@@ -718,7 +718,7 @@ hipError_t launch_tiled_f(const LinearArgs& a, const LinearPlan& p, hipStream_t 
     }
   }
   if (p.bm == 256) {
-    static std::atomic<int> done{0};
+    static SmemAllowed done{0};
     constexpr int sm = (2 * 2 * 256 * 128 > kWoqWaves * 128 * kTileRowBytes) ? 2 * 2 * 256 * 128 : kWoqWaves * 128 * kTileRowBytes;
     auto k = k_woq_gemm256<F, kWoqWaves, WL>;
     hipError_t e = allow_smem(k, sm, done);

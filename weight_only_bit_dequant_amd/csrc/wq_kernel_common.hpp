@@ -2,10 +2,9 @@
 // MFMA wrappers, buffer loads and the output epilogue.
 #pragma once
 
-#include <atomic>
-
 #include "wq_device.hpp"
 #include "wq_internal.hpp"
+#include "wq_smem.hpp"
 
 namespace wq {
 
@@ -267,15 +266,6 @@ __device__ __forceinline__ void tile_store(uint16_t* Y, int M, int N, int mw, in
         if (n + e < N) Y[(int64_t)m * N + n + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
     }
   }
-}
-
-// Dynamic LDS above 64 KiB must be allowed per kernel once per process.
-template <typename Kern>
-hipError_t allow_smem(Kern k, int bytes, std::atomic<int>& done) {
-  if (bytes <= 65536 || done.load(std::memory_order_acquire)) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.store(1, std::memory_order_release);
-  return e;
 }
 
 }  // namespace wq

@@ -561,7 +561,7 @@ hipError_t launch_nosplit(const LinearArgs& a, dim3 grid, hipStream_t s) {
   constexpr int SPW = spw_nosplit<F>() * 12 / NW;
   constexpr int sm = smem_bytes<F, MT, NTW, NW, WL, SPW>(true);
   static_assert(sm <= 160 * 1024, "no-split tile exceeds the LDS of a CU");
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_linear<F, MT, NTW, NW, SPW, true, WL>;
   hipError_t e = allow_smem(k, sm, done);
   if (e != hipSuccess) return e;

@@ -339,14 +339,14 @@ __global__ __launch_bounds__(kWaves * 64) void k_static_mlp2(Mlp2Args a) {
 hipError_t launch_static_mlp2(const Mlp2Args& a, hipStream_t s) {
   const unsigned grid = (unsigned)((a.M + 15) / 16);
   if (a.K1 <= kSpK1 && a.N1 <= kSpN1 && a.N2 <= kSpN2) {
-    static std::atomic<int> done_sp{0};
+    static SmemAllowed done_sp{0};
     hipError_t e = allow_smem(k_static_mlp2_sp, (int)kSpSmem, done_sp);
     if (e != hipSuccess) return e;
     k_static_mlp2_sp<<<grid, kWaves * 64, kSpSmem, s>>>(a);
     return hipGetLastError();
   }
   const size_t sm = mlp2_smem_bytes(a.K1, a.N1, a.N2);
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   hipError_t e = allow_smem(k_static_mlp2, sm > 65536 ? 160 * 1024 : (int)sm, done);
   if (e != hipSuccess) return e;
   k_static_mlp2<<<grid, kWaves * 64, sm, s>>>(a);

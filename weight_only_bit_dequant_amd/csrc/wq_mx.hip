@@ -339,7 +339,7 @@ __global__ __launch_bounds__(kMxMidWaves * 64) void k_mx_mid(LinearArgs a) {
 template <int WL, int NB>
 hipError_t launch_mx_mid_nb(const LinearArgs& a, hipStream_t s) {
   static_assert(kMxMidSmem <= 160 * 1024, "exceeds the LDS of a CU");
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_mx_mid<WL, NB>;
   hipError_t e = allow_smem(k, kMxMidSmem, done);
   if (e != hipSuccess) return e;
@@ -470,7 +470,7 @@ __host__ __device__ constexpr int mx_small_smem(int MT, int K) {
 template <int MT, int WL, int NS>
 hipError_t launch_mx_small_ns(const LinearArgs& a, hipStream_t s) {
   static_assert(mx_small_smem(MT, kMxSmallMaxK) <= 160 * 1024, "exceeds the LDS of a CU");
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_mx_small<MT, WL, NS>;
   hipError_t e = allow_smem(k, mx_small_smem(MT, kMxSmallMaxK), done);
   if (e != hipSuccess) return e;
@@ -1014,18 +1014,14 @@ hipError_t launch_mx_tile(const LinearArgs& a, hipStream_t s) {
   const size_t pre = TT::pre_bytes(a.K);
   constexpr int limit = 128 * 1024;
   if ((a.K / 32) % 16 == 0 && TT::TILES + pre <= (size_t)limit) {
-    static std::atomic<int> done{0};
+    static SmemAllowed done{0};
     const int sm = (int)(TT::TILES + pre);
     auto k = k_mx_gemm_tiled<BM, BN, WGN, true, false, WL>;
-    if (sm > 65536 && !done.load(std::memory_order_acquire)) {
-      hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                         limit);
-      if (e != hipSuccess) return e;
-      done.store(1, std::memory_order_release);
-    }
+    hipError_t e = allow_smem(k, sm > 65536 ? limit : sm, done);
+    if (e != hipSuccess) return e;
     k<<<grid, 128 * WGN, sm, s>>>(a);
   } else {
-    static std::atomic<int> done{0};
+    static SmemAllowed done{0};
     auto k = k_mx_gemm_tiled<BM, BN, WGN, false, false, WL>;
     hipError_t e = allow_smem(k, TT::TILES, done);
     if (e != hipSuccess) return e;
@@ -1037,7 +1033,7 @@ hipError_t launch_mx_tile(const LinearArgs& a, hipStream_t s) {
 template <int BM, int BN, int WL, int WGN = 2>
 hipError_t launch_f8_tile(const LinearArgs& a, hipStream_t s) {
   using TT = MxTile<BM, BN, 128 * WGN, true>;
-  static std::atomic<int> done{0};
+  static SmemAllowed done{0};
   auto k = k_mx_gemm_tiled<BM, BN, WGN, false, true, WL>;
   hipError_t e = allow_smem(k, TT::TILES, done);
   if (e != hipSuccess) return e;
@@ -1050,7 +1046,7 @@ hipError_t launch_f8_gemm_tiled_l(const LinearArgs& a, hipStream_t s) {
   // the largest tiles that still give most CUs a workgroup
   const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   if (t256 >= 192) {
-    static std::atomic<int> done{0};
+    static SmemAllowed done{0};
     hipError_t e = allow_smem(k_f8_gemm256<WL>, kF8Smem, done);
     if (e != hipSuccess) return e;
     k_f8_gemm256<WL><<<dim3((a.N + kF8T - 1) / kF8T, (a.M + kF8T - 1) / kF8T), kF8Waves * 64, kF8Smem, s>>>(a);
@@ -1069,7 +1065,7 @@ hipError_t launch_mx_linear_l(const LinearArgs& a, hipStream_t s) {
     const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
     if (t256 >= 192 && a.K % 128 == 0 && (reinterpret_cast<uintptr_t>(a.xscales) & 3) == 0 &&
         (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0) {
-      static std::atomic<int> done{0};
+      static SmemAllowed done{0};
       hipError_t e = allow_smem(k_mx_gemm256<WL>, kMxSmem, done);
       if (e != hipSuccess) return e;
       k_mx_gemm256<WL><<<dim3((a.N + kMxT - 1) / kMxT, (a.M + kMxT - 1) / kMxT), 1024, kMxSmem, s>>>(a);
