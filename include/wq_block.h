@@ -42,7 +42,8 @@ extern "C" {
 
 /*
  * Quantize bf16 weights W[E][N][K] (contiguous) to codes and scales, one scale
- * for each 128 x 128 block of each of the E matrices.  Any N.
+ * for each 128 x 128 block of each of the E matrices.  Any N; at most 65535
+ * matrices and blocks along N (WQ_EUNSUPPORTED above).
  */
 wq_status wq_block_quantize_weight(const void* W, int64_t E, int64_t N, int64_t K, void* codes, float* scales,
                                    void* stream);
@@ -86,9 +87,17 @@ wq_status wq_block_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int
 /*
  * Block-scaled Linear:
  *   Y[m][n] = bf16( sum_kb Xs[m][kb] Ws[n / 128][kb] sum_{k in kb} Xq[m][k] Wq[n][k] (+ bias[n]) )
- * Each block's products are summed by the FP8 matrix cores in fp32, scaled and
- * added to an fp32 sum; one rounding to bf16.  bias: bf16 [N] or NULL.  Any M
- * and N.  No workspace.
+ * bias: bf16 [N] or NULL.  Any M and N; 0 < K < 2^22.  No workspace.
+ * Precision: the FP8 matrix cores sum a block's 128 products in fp32, but first
+ * align the eight products of each 8 consecutive K to 2^e, e the largest sum of
+ * the exponents of a product's two codes (at least -6 each), and cut what is
+ * below 2^(e - 13) towards zero.  Each of the eight is so off by less than
+ * 2^(e - 13), at most 1/8192 of the largest of them where its codes are normal
+ * numbers.  From there on
+ * it is fp32: Xs * Ws is rounded once, times the block's sum is added to an fp32
+ * sum by one fused multiply-add, and the result is rounded once to bf16.  A
+ * product Xs * Ws beyond fp32's range is infinity (NaN times a block that sums
+ * to zero), one below 2^-126 loses bits.
  */
 wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const void* Wq, const float* Ws,
                           const void* bias, int64_t N, void* Y, void* stream);
@@ -108,7 +117,10 @@ wq_status wq_block_linear(const void* Xq, const float* Xs, int64_t M, int64_t K,
  * of offsets are clamped to [0, T] and the tiles they make to those launched, so
  * no value of them reaches outside Y or the operands (out of order, which rows
  * are written by which expert is not defined).
- * M * K < 2^32 with rows (WQ_EUNSUPPORTED otherwise).
+ * M * K < 2^32 with rows, E <= 2^20, 0 < K < 2^22 (WQ_EUNSUPPORTED otherwise).
+ * The kernel's form goes by T / min(E, T), rows of an expert on average: a much
+ * larger capacity than rows, or one expert with nearly all of them, costs time
+ * (up to a fifth where measured), not precision.
  */
 wq_status wq_block_grouped_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const int32_t* rows,
                                   const int32_t* offsets, int64_t T, int64_t E, const void* Wq, const float* Ws,

@@ -44,13 +44,19 @@ BlockForm block_form(bool grouped, int T, int E, int N, int K) {
   // look for their rows less often.
   const int64_t cols = (N + 15) / 16;
   // Long and narrow: a wave's trips to memory one after the other are the time, so two of its blocks are under way
-  // (4 x 2344 x 7552: 6.05 against 7.0, 16 x 1024 x 16384 9.3 against 10.8, 32 x 2048 x 5632 5.6 against 6.1; not
-  // where the stream itself is: 1 x 4096 x 8192 7.8 against 7.6, 1 x 512 x 8192 5.1 against 5.0).
+  // (4 x 2344 x 7552: 6.05 against 7.0; of 1 row, N = 512, 1024, 2048 and 2560: K = 8192 5.4, 5.5, 5.8 and 6.2 against
+  // 6.4, 6.5, 6.8 and 6.9, K = 16384 8.1 to 9.8 against 9.9 to 11.1; 16 and 32 rows gain 0.7 to 0.9 and 1.3 to 1.4).
+  // Not where the stream itself is the time: N = 4096 gets nothing at K = 8192 and 16384 (1 row 8.0 against 7.9, 12.5
+  // against 12.4) and loses 0.1 to 0.2 below.  The bounds lie inside what was measured, not at its edge: K = 4096 and
+  // 5120 would gain 0.1 to 0.5 too at N <= 2560, and N between 2560 and 4096 is not measured.
   const bool deep = kb >= 44 && N <= 2560;
   if (grouped && rows <= 16) {
     // (1 x 2 of 32, 1440 x 1920: 4.2 against 5.4 with 64 columns; 10 x 1 of 4, 3856 x 3184: 8.4 against 8.9 with 32 and
     // 10.5 with 64; 6 x 2 of 16, 928 x 544: 4.2 with 32 against 4.6; 16 x 4 of 32, 2048 x 2048: 15.2 with 32, 16.6 with
-    // 64, 17.2 with 16; 128 x 4 of 64, 1536 x 2048: 29.0 with 64, 30.7 with 32, 44 with 16, 30 in 256 x 128 tiles)
+    // 64, 17.2 with 16; 128 x 4 of 64, 1536 x 2048: 29.0 with 64, 30.7 with 32, 44 with 16, 30 in 256 x 128 tiles.
+    // 32 and 64 columns are close: with 4608 to 6144 tiles, 4 rows each of 64 experts, 64 are 0 to 5 % behind)
+    // What this rule does not see is how uneven the experts are, and that T may be more than there are rows: 1024 rows
+    // of 64 experts, 1536 x 2048, take 42.5 evenly and 50.6 where one has 961 of them (256 x 128 tiles 44.4).
     const int64_t tiles = cols * groups;
     if (tiles <= 256 && deep) return kStream16Deep;
     if (tiles <= 256 || (tiles < 1024 && kb >= 16)) return kStream16;
@@ -68,6 +74,7 @@ BlockForm block_form(bool grouped, int T, int E, int N, int K) {
     if (tiles <= 1024 || rows <= 16) return kStream32;
     return kStream32x32;
   }
+  // (T = 8192 with 200 rows of 64 experts takes 39.2 in 256 x 128 tiles, 33.1 in the stream that T = 200 gets.)
   // More rows: the form with the least time, but no less than the memory's (weights, for experts those of all that
   // have rows), where the widest does best: fewer workgroups look for their rows (31 rows each of 64 experts, 1536 x
   // 2048: 45 with 256 x 128 tiles against 52-56 with the others).

@@ -76,11 +76,12 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
   return u32x2{e4m3_pack4(q.v[0], q.v[1], q.v[2], q.v[3]), e4m3_pack4(q.v[4], q.v[5], q.v[6], q.v[7])};
 }
 
-// silu(g) u = g / (1 + exp(-g)) u within a few fp32 ulp.
-//   exp(-g) = 2^t, t = -g log2 e in two parts, the hardware's 2^x for what is
-//   left of them beside a whole number;
-//   the quotient is g' r with one correction by its remainder, r the hardware's
-//   reciprocal of d' (1 ulp).  d' = 2^-8 (1 + exp(-g)) and g' = 2^-8 g: r stays a
+// silu(g) u = g / (1 + exp(-g)) u within a few fp32 ulp (of the fp32 formula's own
+// rounding size; a code may fall to either side of a tie of both).
+//   exp(-g) = 2^t, t = -g log2 e with the constant in two parts (Cody and
+//   Waite's reduction), the hardware's 2^x for what is left beside a whole number;
+//   the quotient is g' r with one correction by its remainder (a Newton step on
+//   the quotient), r the hardware's reciprocal of d' (1 ulp).  d' = 2^-8 (1 + exp(-g)) and g' = 2^-8 g: r stays a
 //   normal number up to the largest d (reciprocals below 2^-126 read as 0).
 // Below -88.6 exp(-g) leaves fp32 and the result is -0 (its size is below
 // 3e-37); above 90 exp(-g) no longer counts and the result is g.  Both are g
@@ -88,7 +89,7 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, float s) {
 // infinity) and NaN give NaN: the quotient's correction would make NaN of both
 // infinities.
 // Two library calls (expf and division) took 45 instructions an element, more
-// than the memory's time (8192 x 8192: 75 us; so 65.5).
+// than the memory's time (8192 x 8192: 75 us; so 63 to 67.5).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float L = -1.4426950216293335f, Ll = -1.9259629911e-8f;  // -log2 e = L + Ll
   constexpr float far = -88.6f;
@@ -108,8 +109,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // ---------------------------------------------------------------- activation rows, gated activation
 // One lane per 8 elements, one 16-lane row per scale block; the blocks of all
 // rows are numbered through, so short rows share a workgroup.  Bound by memory:
-// the gate over 8192 x 8192 moves its 338 MB in 65.5 us, 5.2 TB/s (a copy of
-// that size 4.8); non-temporal loads, 512 threads and two blocks to a lane were
+// the gate over 8192 x 8192 moves its 338 MB in 63 to 67.5 us, 5.0 to 5.3 TB/s (a
+// copy of that size 4.8); non-temporal loads, 512 threads and two blocks to a lane were
 // no faster.  64 x 2048 takes 2.6 us, 1 above an empty launch: one trip.
 // The row of a block is blk / KB as a product: with 2^sh < KB <= 2^(sh + 1) and
 // magic = ceil(2^(32 + sh) / KB), exact for blk < 2^31 (KB = 1: magic = 0).
@@ -145,8 +146,8 @@ __global__ __launch_bounds__(256) void k_block_quant_rows(const uint16_t* __rest
 // its one write: lane l of wave w holds chunks w * 64 + l + 64 * WPR * j
 // (8 elements each) for j < CPT, so its 16-lane rows are scale blocks.  The
 // sum of squares crosses lanes by shuffles and waves through LDS.  Bound by
-// memory: 16384 x 8192 moves 941 MB in 160 us, 5.9 TB/s (a copy 4.8; two passes
-// over a row would read 537 MB again); a row of 4096 takes 2.6 us, one trip and
+// memory: 16384 x 8192 moves 941 MB in 160 to 164 us, 5.7 to 5.9 TB/s (a copy 4.8; two passes
+// over a row would read 537 MB again); a row of 4096 takes 2.6 to 3.0 us, one trip and
 // one meeting of its waves above an empty launch (1.6 us).
 template <int WPR>
 constexpr int norm_rows() {  // rows per workgroup: four waves or one row
@@ -275,8 +276,9 @@ static hipError_t norm_launch(const BlockNormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
-  // The narrowest form that holds a row, more waves before more chunks: a row of 8192 in 8 waves x 2 chunks takes
-  // 163 us against 166 in 4 x 4 and 179 in 16 x 1 (16384 rows), 3.7 against 4.3 us (64 rows).
+  // The narrowest form that holds a row: one chunk to a lane in up to 6 waves (rows to 3072), two in 4 to 8 (to 8192),
+  // four above.  A row of 8192 in 8 waves x 2 chunks takes 163 us against 166 in 4 x 4 and 179 in 16 x 1 (16384 rows),
+  // 3.7 against 4.3 us (64 rows).
   const int chunks = (a.K + 127) / 128 * 16;  // whole 16-lane rows
   if (chunks <= 64) return norm_launch<1, 1>(a, s);
   if (chunks <= 128) return norm_launch<2, 1>(a, s);
