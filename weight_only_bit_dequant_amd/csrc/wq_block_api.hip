@@ -3,35 +3,19 @@
 #include <hip/hip_runtime_api.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
+#include "wq_api_checks.hpp"
 #include "wq_block.h"
 #include "wq_block_internal.hpp"
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 30;
+using namespace wq::api;
+
 constexpr int64_t kMaxGrid = 65535;  // workgroups along y and z
 // Scale blocks of a row operator's result: at most 32 threads for each (64 for
 // a row of one), and a launch holds fewer than 2^32.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 27;
-
-wq_status fail(wq_status st, const char* fmt, ...) {
-  char text[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(text, sizeof(text), fmt, ap);
-  va_end(ap);
-  return wq::api_error(st, text);
-}
-
-wq_status launched(hipError_t e, const char* what) {
-  if (e == hipErrorInvalidConfiguration) return fail(WQ_EUNSUPPORTED, "%s: more tiles than a launch holds", what);
-  return e == hipSuccess ? wq::api_ok() : fail(WQ_EHIP, "%s launch: %s", what, hipGetErrorString(e));
-}
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 // sizes every call has: `what` names the entry point in messages
 wq_status check_sizes(const char* what, int64_t M, int64_t K) {

@@ -6,17 +6,12 @@
 //
 // The module holds no state but the C functions' addresses, which bind() takes
 // from the library that wq.lib() loaded.
-#include <c10/hip/HIPFunctions.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <optional>
-#include <sstream>
-#include <stdexcept>
-
 #include "wq_block.h"
+#include "wq_py.hpp"
 
 namespace {
+
+using namespace wq_py;
 
 decltype(&wq_block_quantize_act) p_quantize_act;
 decltype(&wq_block_silu_mul_quantize) p_silu_mul_quantize;
@@ -24,82 +19,11 @@ decltype(&wq_block_add_rmsnorm_quantize) p_add_rmsnorm_quantize;
 decltype(&wq_block_linear) p_linear;
 decltype(&wq_block_grouped_linear) p_grouped_linear;
 
-// What Python raises as ValueError.
-struct Refused : std::runtime_error {
-  using std::runtime_error::runtime_error;
-};
-
-const at::Tensor& tensor(PyObject* o, const char* name) {
-  if (!THPVariable_Check(o)) throw Refused(std::string(name) + " must be a tensor");
-  return THPVariable_Unpack(o);
-}
-
-[[noreturn]] void refuse(const at::Tensor& t, const char* name, const std::string& want) {
-  std::ostringstream s;
-  s << name << " must be " << want << " (got " << t.scalar_type() << " " << t.sizes() << ", strides " << t.strides()
-    << ", on " << t.device() << ")";
-  throw Refused(s.str());
-}
-
-// A contiguous tensor of this type, shape and device: its data.
-void* data(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
-  if (t.scalar_type() != type || t.sizes() != shape || t.device() != dev || !t.is_contiguous()) {
-    std::ostringstream s;
-    s << "a contiguous " << type << " tensor of shape " << shape << " on " << dev;
-    refuse(t, name, s.str());
-  }
-  return t.data_ptr();
-}
-
-void* data(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
-  return data(tensor(o, name), name, type, shape, dev);
-}
-
-void* data_or_null(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
-  return o == Py_None ? nullptr : data(o, name, type, shape, dev);
-}
-
-// A bf16 matrix on the GPU whose rows are contiguous.
-struct Rows {
-  const void* p;
-  int64_t M, K, ld;
-  c10::Device dev;
-};
-Rows rows(PyObject* o, const char* name) {
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kBFloat16 || t.dim() != 2 || !t.is_cuda() || (t.size(1) > 1 && t.stride(1) != 1))
-    refuse(t, name, "a bf16 matrix with contiguous rows on the GPU");
-  // a single row's stride says nothing
-  return {t.data_ptr(), t.size(0), t.size(1), t.size(0) > 1 ? t.stride(0) : t.size(1), t.device()};
-}
-
 constexpr int64_t kb(int64_t n) { return (n + WQ_BLOCK - 1) / WQ_BLOCK; }
 
-// Runs `call(stream)` on the device's current stream with the device current.
-template <typename F>
-wq_status on(c10::Device dev, F&& call) {
-  const c10::DeviceIndex was = c10::hip::current_device();
-  if (was != dev.index()) c10::hip::set_device(dev.index());
-  const wq_status st = call((void*)c10::hip::getCurrentHIPStream(dev.index()).stream());
-  if (was != dev.index()) c10::hip::set_device(was);
-  return st;
-}
-
-// Entry: `n` arguments, C++ exceptions turned into Python's.
 template <typename F>
 PyObject* entry(Py_ssize_t given, Py_ssize_t n, F&& body) {
-  try {
-    if (given != n) throw std::invalid_argument("wrong number of arguments");
-    if (!p_linear) throw std::logic_error("bind() has not been called");
-    return PyLong_FromLong(body());
-  } catch (const Refused& e) {
-    PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
-  }
-  return nullptr;
+  return wq_py::entry(p_linear != nullptr, given, n, body);
 }
 
 template <typename Fn>
@@ -193,27 +117,10 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // bind(quantize_act, silu_mul_quantize, add_rmsnorm_quantize, linear, grouped_linear): addresses of the C functions
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind() takes five addresses");
-    return nullptr;
-  }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
-    p[i] = PyLong_AsVoidPtr(a[i]);
-    if (!p[i]) {
-      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
-      return nullptr;
-    }
-  }
-  p_quantize_act = (decltype(p_quantize_act))p[0];
-  p_silu_mul_quantize = (decltype(p_silu_mul_quantize))p[1];
-  p_add_rmsnorm_quantize = (decltype(p_add_rmsnorm_quantize))p[2];
-  p_linear = (decltype(p_linear))p[3];
-  p_grouped_linear = (decltype(p_grouped_linear))p[4];
-  Py_RETURN_NONE;
+  return bind_all(a, n, {(void**)&p_quantize_act, (void**)&p_silu_mul_quantize, (void**)&p_add_rmsnorm_quantize,
+                         (void**)&p_linear, (void**)&p_grouped_linear});
 }
 
-#define WQ_METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {WQ_METHOD(bind),   WQ_METHOD(quantize_act),   WQ_METHOD(silu_mul_quantize), WQ_METHOD(add_rmsnorm_quantize),
                          WQ_METHOD(linear), WQ_METHOD(grouped_linear), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_call", "Calls of the block-scaled FP8 operators.", -1, methods,
