@@ -1,0 +1,323 @@
+"""The experts' routing on the GPU against the oracle: experts, order and places
+exactly, weights and sums with derived bounds."""
+
+import numpy as np
+import pytest
+import torch
+
+from int8_bound import U, sum_bound
+from oracle import experts as X
+from test_gpu_block import DEV, case, host
+
+experts = pytest.importorskip("weight_only_bit_dequant_amd.experts")
+
+pytestmark = pytest.mark.gpu
+
+# Weights: from fp64 scores and one rounding to fp32, 1 u (the oracle's own fp64 arithmetic far below).
+REL64 = U * (1 + 2.0**-20)
+# Where a softmax sum is fp32 (not renormalised, choices by logit): a term e^-d is off by u d (the difference rounded)
+# and 4 u (the exponential) of itself, the mean of d under the softmax is at most ln E < 7, at most 22 additions u each;
+# then the quotient's and the result's rounding: 7 + 4 + 22 + 2 < 40 u.
+REL32 = 40 * U
+
+
+def logits_of(M, E, seed, half=False):
+    g = torch.Generator().manual_seed(seed)
+    l = 1.5 * torch.randn(M, E, generator=g) + torch.randn(E, generator=g)
+    return l.to(torch.bfloat16) if half else l
+
+
+def check_route(logits, top, valid=None, bias=None, **kw):
+    """route() of CPU logits against the oracle; returns the Routing."""
+    M, E = logits.shape
+    args = dict(kind=kw.get("score", "softmax"), groups=kw.get("groups", 1), keep=kw.get("keep_groups"),
+                pairs=kw.get("group_score", "max") == "top2", renormalize=kw.get("renormalize", True), scale=kw.get("scale", 1.0))
+    ids, w, off, rows, places = X.route(logits.double().numpy(), top, valid=None if valid is None else valid.numpy(),
+                                        bias=None if bias is None else bias.numpy(), **args)
+    out = experts.buffers(M, E, top, DEV)
+    for t in out:
+        t.fill_(-77)
+    l = logits.to(DEV) if logits.is_contiguous() else torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=DEV).copy_(logits)
+    r = experts.route(l, top, valid=None if valid is None else valid.to(DEV), bias=None if bias is None else bias.to(DEV), out=out, **kw)
+    assert np.array_equal(host(r.ids), ids)
+    assert np.array_equal(host(r.offsets), off) and np.array_equal(host(r.places), places)
+    assert np.array_equal(host(r.rows)[: len(rows)], rows) and (host(r.rows)[len(rows):] == -77).all()
+    got = host(r.weights).astype(np.float64)
+    narrow = args["kind"] == "softmax" and not args["renormalize"] and bias is None and not (args["pairs"] and args["groups"] > 1)
+    assert np.array_equal(np.isnan(got), np.isnan(w))
+    with np.errstate(invalid="ignore"):
+        bad = np.abs(got - w) > (REL32 if narrow else REL64) * np.abs(w) + 2.0**-149
+    assert not bad.any(), np.abs(got / w - 1)[bad].max()
+    return r
+
+
+MODES = {
+    "softmax": dict(),
+    "softmax as it is": dict(renormalize=False),
+    "sigmoid": dict(score="sigmoid", scale=2.5),
+    "sigmoid as it is": dict(score="sigmoid", renormalize=False),
+    "bias": dict(score="sigmoid", bias=True),
+    "softmax bias": dict(bias=True, renormalize=False),
+}
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("M,E,top", [(1, 1, 1), (1, 8, 2), (3, 16, 16), (5, 17, 3), (40, 60, 4), (64, 64, 6), (65, 128, 8), (33, 160, 6),
+                                     (130, 256, 8), (7, 300, 9), (200, 512, 32), (9, 1000, 17), (70, 1024, 10)])
+def test_route(mode, half, M, E, top):
+    case(f"route {mode} half={half} {M} of {E} top {top}")
+    kw = dict(MODES[mode])
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E)) if kw.pop("bias", False) else None
+    valid = torch.rand(M, generator=torch.Generator().manual_seed(M)) < 0.8 if M % 2 else None
+    check_route(logits_of(M, E, M + E, half), top, valid=valid, bias=bias, **kw)
+
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M,E,top,G,keep", [(20, 16, 4, 2, 1), (9, 16, 4, 16, 5), (30, 256, 8, 8, 4), (70, 160, 6, 8, 3), (12, 60, 5, 4, 2),
+                                            (11, 60, 5, 3, 2), (13, 60, 8, 12, 5), (66, 320, 8, 16, 4), (8, 1024, 16, 64, 9), (10, 96, 4, 32, 7),
+                                            (21, 1000, 20, 8, 3), (6, 490, 8, 7, 7), (5, 63, 2, 63, 9), (4, 64, 3, 64, 3), (300, 36, 6, 6, 3)])
+def test_route_groups(group_score, bias, M, E, top, G, keep):
+    case(f"route groups {group_score} bias={bias} {M} of {E} top {top} {keep} of {G}")
+    b = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)) if bias else None
+    check_route(logits_of(M, E, M * E, E % 3 == 0), top, bias=b, groups=G, keep_groups=keep, group_score=group_score,
+                score="sigmoid" if M % 2 else "softmax", renormalize=M % 3 != 0)
+
+
+@pytest.mark.parametrize("M,E,top", [(64, 8, 2), (65, 8, 2), (128, 8, 1), (1000, 60, 4), (5000, 128, 8), (16500, 8, 2), (40000, 16, 1), (17000, 1024, 2)])
+def test_route_many_tokens(M, E, top):
+    """One stretch of tokens and one more, stretches of several passes, a short last one."""
+    case(f"route many {M} of {E} top {top}")
+    valid = torch.rand(M, generator=torch.Generator().manual_seed(M)) < 0.9
+    valid[M - M // 9:] = False
+    check_route(logits_of(M, E, M, True), top, valid=valid)
+
+
+def test_route_one_expert_takes_all():
+    case("route one expert takes all")
+    l = logits_of(300, 32, 5)
+    l[:, 7] = 50.0
+    r = check_route(l, 3)
+    assert int(r.offsets[8] - r.offsets[7]) == 300
+
+
+def test_route_ties_masks_and_nan():
+    case("route ties, masks, NaN")
+    inf, nan = float("inf"), float("nan")
+    l = torch.zeros(16, 40)
+    l[1] = -inf
+    l[2, 5:], l[2, :5] = -inf, torch.tensor([1.0, 3.0, 3.0, 2.0, 3.0])
+    l[3, 39] = -0.0
+    l[4, 20] = nan
+    l[5, [3, 30]] = inf
+    l[6] = torch.finfo(torch.float32).min
+    l[7] = torch.finfo(torch.float32).min
+    l[7, [11, 12]] = 1.0
+    l[8, ::2] = -inf
+    l[9] = torch.arange(40) * -30.0          # scores down to e^-1170
+    l[10] = torch.arange(40) * 30.0 - 600.0
+    l[11] = nan
+    l[12], l[12, 17] = -inf, nan
+    l[13], l[13, 17] = -inf, inf
+    l[14] = torch.finfo(torch.float32).max
+    l[15] = -200.0
+    for kw in (dict(), dict(renormalize=False), dict(score="sigmoid"), dict(score="sigmoid", renormalize=False), dict(groups=5, keep_groups=2),
+               dict(groups=8, keep_groups=2), dict(groups=8, keep_groups=3, group_score="top2", score="sigmoid"), dict(groups=10, keep_groups=1, group_score="top2")):
+        for top in (1, 6):
+            check_route(l, top, **kw)
+            bias = torch.linspace(-1, 1, 40)
+            bias[[4, 9]] = -inf
+            check_route(l, top, bias=torch.zeros(40), **kw)
+            check_route(l, top, bias=bias, **kw)
+    bias[11] = nan
+    check_route(l, 3, bias=bias)
+
+
+def test_route_strides():
+    case("route strides")
+    for half in (False, True):
+        l = logits_of(100, 75, 3, half)
+        for part in (l[:, :60], l[:, 3:70], l[::2, 1:65]):
+            check_route(part, 5)
+            check_route(part[:1], 5)
+
+
+def test_route_no_tokens():
+    case("route no tokens")
+    r = experts.route(torch.empty(0, 12, device=DEV), 3)
+    assert r.ids.shape == (0, 3) and r.rows.numel() == 0 and host(r.offsets).tolist() == [0] * 13
+    r = experts.route(torch.zeros(200, 12, device=DEV), 3, valid=torch.zeros(200, dtype=torch.bool, device=DEV))
+    assert host(r.offsets).tolist() == [0] * 13 and bool((r.ids == -1).all()) and bool((r.weights == 0).all())
+
+
+def test_route_near_choices():
+    """Choices that fp32 would not tell apart: equal scores, biases a few 2^-30 from each other."""
+    case("route near choices")
+    E = 64
+    g = torch.Generator().manual_seed(4)
+    l = torch.full((50, E), 0.75)
+    bias = (torch.randperm(E, generator=g).float() - 32) * 2.0**-30
+    check_route(l, 8, bias=bias, score="sigmoid")
+    check_route(l, 8, bias=bias)
+
+
+# ---------------------------------------------------------------- combine
+
+
+def check_combine(M, top, N, T, base, seed=1, scatter=False):
+    g = torch.Generator().manual_seed(seed + M + N)
+    y = torch.randn(T, N, generator=g).to(torch.bfloat16)
+    places = torch.randint(-1, T, (M, top), generator=g, dtype=torch.int32) if T else torch.full((M, top), -1, dtype=torch.int32)
+    if scatter:
+        places.view(-1)[::3] = T + 5
+        places.view(-1)[1::7] = -(1 << 31)
+    w = torch.randn(M, top, generator=g)
+    b = torch.randn(M, N, generator=g).to(torch.bfloat16) if base else None
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    got = experts.combine(y.to(DEV), places.to(DEV), w.to(DEV), base=None if b is None else b.to(DEV), out=out)
+    ref, size = X.combine(y.double().numpy(), places.numpy(), w.numpy(), None if b is None else b.double().numpy())
+    off = np.abs(got.double().cpu().numpy() - ref)
+    assert (off <= sum_bound(ref, size, top)).all()
+
+
+@pytest.mark.parametrize("base", [False, True])
+@pytest.mark.parametrize("M,top,N,T", [(1, 1, 8, 1), (1, 8, 4096, 8), (3, 2, 7, 5), (5, 4, 513, 20), (17, 6, 520, 40), (33, 3, 2056, 60), (64, 8, 1000, 512),
+                                       (200, 5, 72, 3), (9, 32, 264, 100), (2, 40, 1025, 9), (300, 2, 2048, 600)])
+def test_combine(base, M, top, N, T):
+    case(f"combine {M}x{top}x{N} of {T} base={base}")
+    check_combine(M, top, N, T, base)
+    check_combine(M, top, N, T, base, seed=2, scatter=True)
+
+
+def test_combine_edges():
+    case("combine edges")
+    check_combine(4, 3, 24, 0, True)
+    check_combine(4, 3, 25, 0, False)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    y, places, w = torch.full((2, 16), float("nan"), **bf), torch.full((3, 2), -1, dtype=torch.int32, device=DEV), torch.full((3, 2), float("nan"), device=DEV)
+    base = torch.ones(3, 16, **bf)
+    # rows that no choice names are not read into the sum, nor their weights; the result may take the base's place
+    out = experts.combine(y, places, w, base=base, out=base)
+    assert out is base and bool((base == 1).all())
+    assert experts.combine(y, places[:, :0], w[:, :0]).eq(0).all()
+    assert experts.combine(y, places[:0], w[:0]).shape == (0, 16)
+    # a named row's NaN arrives, under a weight of zero too
+    places[1, 1], w[1, 1] = 1, 0.0
+    out = experts.combine(y, places, w, base=base)
+    assert bool(out[1].isnan().all()) and bool((out[[0, 2]] == 1).all())
+
+
+def test_combine_past_32_bit_offsets():
+    """Rows of Y from byte 2^32 on."""
+    case("combine past 2^32 bytes")
+    N, T = 8192, 300_000
+    y = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV)
+    y[-3:] = torch.randn(3, N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    places = torch.tensor([[T - 1, 0], [T - 2, T - 3]], dtype=torch.int32, device=DEV)
+    out = experts.combine(y, places, torch.ones(2, 2, device=DEV))
+    assert torch.equal(out[0], y[-1]) and torch.equal(out[1], (y[-2].float() + y[-3].float()).to(torch.bfloat16))
+
+
+# ---------------------------------------------------------------- use
+
+
+def test_same_again_on_other_streams_and_in_graphs():
+    """Two graphs and an eager call in turn, each with a workspace of its own; inputs change between replays."""
+    case("route, combine: repeat, stream, graphs")
+    M, E, top, N = 700, 48, 4, 264
+    logits, y = logits_of(M, E, 1).to(DEV), torch.randn(M * top, N, device=DEV).to(torch.bfloat16)
+    other = logits_of(M, E, 2).to(DEV)
+
+    def step(l):
+        r = experts.route(l, top)
+        return [*r, experts.combine(y, r.places, r.weights)]
+
+    want = {k: [host(t).copy() for t in step(l)] for k, l in (("a", logits), ("b", other))}
+
+    def same(k, got):
+        return all(np.array_equal(u, host(v)) for u, v in zip(want[k], got))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = step(logits)
+    torch.cuda.current_stream().wait_stream(s)
+    assert same("a", got)
+    fed = logits.clone()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(fed)
+        graphs.append((g, out))
+    for k, l in (("a", logits), ("b", other), ("a", logits)):
+        fed.copy_(l)
+        for g, out in graphs:
+            g.replay()
+        assert same("a", step(logits))
+        for g, out in graphs:
+            assert same(k, out)
+
+
+def test_workspace():
+    case("route workspace")
+    l = logits_of(500, 60, 3).to(DEV)
+    need = experts.workspace_bytes(500, 60)
+    assert need > 0 and experts.workspace_bytes(64, 60) == 0
+    want = experts.route(l, 4)
+    dirty = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        got = experts.route(l, 4, workspace=dirty)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    with pytest.raises(ValueError):
+        experts.route(l, 4, workspace=dirty[: need - 4])
+
+
+def test_refusals():
+    case("experts refusals")
+    l = logits_of(6, 12, 1).to(DEV)
+    b = experts.buffers(6, 12, 2, DEV)
+    f32 = dict(device=DEV)
+    y = torch.zeros(5, 16, dtype=torch.bfloat16, device=DEV)
+    places, w = torch.zeros(6, 2, dtype=torch.int32, device=DEV), torch.zeros(6, 2, device=DEV)
+    bad = [
+        lambda: experts.route(l.double(), 2),
+        lambda: experts.route(l.half(), 2),
+        lambda: experts.route(l.cpu(), 2),
+        lambda: experts.route(l[0], 2),
+        lambda: experts.route(l.t(), 2),
+        lambda: experts.route(l[:1].expand(6, 12), 2),           # rows on top of each other
+        lambda: experts.route(l, 0),
+        lambda: experts.route(l, 13),
+        lambda: experts.route(l, 2.0),
+        lambda: experts.route(l, 3, out=b),
+        lambda: experts.route(l, 2, score="tanh"),
+        lambda: experts.route(l, 2, group_score="mean"),
+        lambda: experts.route(l, 2, bias=torch.zeros(11, **f32)),
+        lambda: experts.route(l, 2, bias=torch.zeros(12)),
+        lambda: experts.route(l, 2, bias=torch.zeros(12, dtype=torch.bfloat16, **f32)),
+        lambda: experts.route(l, 2, groups=5),
+        lambda: experts.route(l, 2, groups=0),
+        lambda: experts.route(l, 2, groups=3, keep_groups=4),
+        lambda: experts.route(l, 2, groups=3, keep_groups=0),
+        lambda: experts.route(l, 2, valid=torch.ones(5, dtype=torch.bool, **f32)),
+        lambda: experts.route(l, 2, valid=torch.ones(6, **f32)),
+        lambda: experts.route(l, 2, scale="x"),
+        lambda: experts.route(l, 2, out=b._replace(ids=b.ids.long())),
+        lambda: experts.route(l, 2, out=b._replace(rows=b.rows[:-1])),
+        lambda: experts.route(torch.zeros(2, 1025, **f32), 2),
+        lambda: experts.route(torch.zeros(2, 64, **f32), 33),
+        lambda: experts.combine(y.float(), places, w),
+        lambda: experts.combine(y[:, ::2], places, w),
+        lambda: experts.combine(y, places.long(), w),
+        lambda: experts.combine(y, places, w[:, :1].contiguous()),
+        lambda: experts.combine(y, places, w.double()),
+        lambda: experts.combine(y, places, w, base=y),
+        lambda: experts.combine(y, places, w, out=torch.empty(6, 16, **f32)),
+        lambda: experts.combine(y, places.cpu(), w),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("not refused:", i)

@@ -2,8 +2,9 @@
 
 Usage: python -m weight_only_bit_dequant_amd.build  (or __graft_entry__.build()).
 Each source is compiled to an object in parallel, then linked into
-weight_only_bit_dequant_amd/libwq.so; beside it _block_call.so, the CPython
-entry points of block.py, is built against torch's headers.
+weight_only_bit_dequant_amd/libwq.so; beside it the CPython entry points of
+block.py, int8.py and experts.py (_block_call.so and so on) are built against
+torch's headers.
 """
 
 import concurrent.futures
@@ -19,10 +20,12 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libwq.so")
-EXT = os.path.join(HERE, "_block_call.so")
+EXTS = {os.path.join(HERE, "_%s_call.so" % name): "wq_%s_py.cpp" % name for name in ("block", "int8", "experts")}
 
 SOURCES = ["wq_api.hip", "wq_plan.cpp", "wq_quant.hip", "wq_linear.hip", "wq_gemm_tiled.hip", "wq_gemm_mid.hip", "wq_mx.hip", "wq_mlp.hip", "wq_noalloc.hip",
-           "wq_block_api.hip", "wq_block_plan.cpp", "wq_block_quant.hip", "wq_block_gemm.hip"]
+           "wq_block_api.hip", "wq_block_plan.cpp", "wq_block_quant.hip", "wq_block_gemm.hip",
+           "wq_int8_api.hip", "wq_int8_quant.hip", "wq_int8_gemm.hip",
+           "wq_experts_api.hip", "wq_experts_route.hip", "wq_experts_combine.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 
@@ -52,32 +55,32 @@ def _compile(src):
     return obj
 
 
-def _build_ext():
-    """_block_call.so: host code only, against the headers and libraries of the torch that will load it."""
+def _build_ext(ext):
+    """CPython entry points: host code only, against the headers and libraries of the torch that will load them."""
     import torch
     from torch.utils import cpp_extension
 
-    tmp = EXT + ".tmp"
+    tmp = ext + ".tmp"
     rocm = cpp_extension.ROCM_HOME or "/opt/rocm"
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE]
     for path in [*cpp_extension.include_paths(), os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "wq_block_py.cpp"), "-o", tmp, "-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    cmd += [os.path.join(CSRC, EXTS[ext]), "-o", tmp, "-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("building _block_call failed:\n%s\n%s" % (" ".join(cmd), r.stderr[-8000:]))
-    os.replace(tmp, EXT)
-    return EXT
+        raise RuntimeError("building %s failed:\n%s\n%s" % (ext, " ".join(cmd), r.stderr[-8000:]))
+    os.replace(tmp, ext)
+    return ext
 
 
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(_build_ext)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + len(EXTS)) as ex:
+        exts = [ex.submit(_build_ext, ext) for ext in EXTS]
         objs = list(ex.map(_compile, SOURCES))
-        ext = ext.result()
+        exts = [ext.result() for ext in exts]
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -86,7 +89,8 @@ def build(verbose=False):
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB)
-        print("built", ext)
+        for ext in exts:
+            print("built", ext)
     return LIB
 
 
