@@ -24,7 +24,7 @@ EXTS = {os.path.join(HERE, "_%s_call.so" % name): "wq_%s_py.cpp" % name for name
 
 SOURCES = ["wq_api.hip", "wq_plan.cpp", "wq_quant.hip", "wq_linear.hip", "wq_gemm_tiled.hip", "wq_gemm_mid.hip", "wq_mx.hip", "wq_mlp.hip", "wq_noalloc.hip",
            "wq_block_api.hip", "wq_block_plan.cpp", "wq_block_quant.hip", "wq_block_gemm.hip",
-           "wq_int8_api.hip", "wq_int8_quant.hip", "wq_int8_gemm.hip",
+           "wq_int8_api.hip", "wq_int8_plan.cpp", "wq_int8_quant.hip", "wq_int8_gemm.hip",
            "wq_experts_api.hip", "wq_experts_route.hip", "wq_experts_combine.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -26,4 +26,16 @@ struct Int8GemmArgs {
 };
 hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s);
 
+// Kernel forms of the products: dot products for single rows (by a wave's columns), streams of the weights for few
+// (by columns x rows of a workgroup; deep: two blocks of a wave under way), LDS tiles for more.
+enum Int8Form {
+  kI8Dot2, kI8Dot4, kI8Dot8, kI8Stream16, kI8Stream16Deep, kI8Stream32,
+  kI8Tile256, kI8Tile256x128, kI8Tile128, kI8Tile128x64, kI8Tile64, kI8Tile32x64, kI8Forms
+};
+// The form of T rows of Y over E experts (a plain Linear: grouped false), chosen on the host (wq_int8_plan.cpp).
+Int8Form int8_form(bool grouped, int T, int E, int N, int K);
+
 }  // namespace wq
+
+// The form's name, for tests (E = 0: a plain Linear).
+extern "C" const char* wq_int8_form(int64_t T, int64_t E, int64_t N, int64_t K);
