@@ -47,7 +47,7 @@ enum {
  *   Scores that a bias or pairs compare, and weights' ratios, are held in fp64;
  *   a softmax sum that only weights need in fp32.
  *
- *   logits   : fp32 (logit_bits 32) or bf16 (16), row m at logits + m * ld elements, ld >= E
+ *   logits   : fp32 (logit_bits 32) or bf16 (16), row m at logits + m * ld elements, E <= ld < 2^22
  *   bias     : fp32 [E] or NULL
  *   valid    : uint8 [M] or NULL; a token with 0 gets no expert
  *   ids      : int32 [M][top]; -1 where fewer than `top` can be picked

@@ -35,6 +35,7 @@ wq_status wq_experts_route(const void* logits, int logit_bits, int64_t ld, int64
   if (!aligned(offsets, 4)) return fail(WQ_EALIGN, "%s: pointers must be aligned to their type", what);
   if (M > 0) {
     if (!logits || !ids || !weights || !rows || !places) return fail(WQ_EINVAL, "%s: null pointer", what);
+    if (ld >= 1 << 22) return fail(WQ_EUNSUPPORTED, "%s: row stride of 2^22 or more", what);
     if (ld < E) return fail(WQ_EINVAL, "%s: row stride %lld is shorter than a row", what, (long long)ld);
     if (!aligned(logits, logit_bits / 8) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
         !aligned(rows, 4) || !aligned(places, 4) || !aligned(workspace, 4))

@@ -16,6 +16,9 @@
 // take one launch of one workgroup; more take two: the first writes counts of
 // each stretch of tokens, in the second each workgroup adds up the counts before
 // its own.
+#include <type_traits>
+#include <utility>
+
 #include "wq_experts_internal.hpp"
 #include "wq_row_tiles.hpp"
 
@@ -28,69 +31,181 @@ constexpr uint16_t kNone = 0xFFFF;
 
 // ---------------------------------------------------------------- keys
 
-__device__ __forceinline__ uint32_t key_of(float c) {
-  const uint32_t u = fbits(c + 0.0f);  // -0 is 0
-  return c != c ? ~0u : c == -__builtin_inff() ? 0u : u ^ (uint32_t)(((int32_t)u >> 31) | (int32_t)0x80000000);
-}
-__device__ __forceinline__ uint64_t key_of(double c) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, c + 0.0);
-  return c != c ? ~0ull : c == -__builtin_inf() ? 0ull : u ^ (uint64_t)(((int64_t)u >> 63) | (int64_t)0x8000000000000000ull);
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  const uint32_t u = k ^ (k >> 31 ? 0x80000000u : ~0u);
-  return k == ~0u ? __builtin_nanf("") : k == 0 ? -__builtin_inff() : bitsf(u);
-}
-__device__ __forceinline__ double value_of(uint64_t k) {
-  const uint64_t u = k ^ (k >> 63 ? 0x8000000000000000ull : ~0ull);
-  return k == ~0ull ? __builtin_nan("") : k == 0 ? -__builtin_inf() : __builtin_bit_cast(double, u);
-}
-
-// Over the first `n` (a power of two) of the lanes that share lane / n.
-template <typename T>
-__device__ __forceinline__ T max_over(T v, int n) {
-  for (int d = 1; d < n; d <<= 1) {
-    const T o = __shfl_xor(v, d);
-    v = v > o ? v : o;
+// Logits as integers in their order: 0 for -infinity (not to be picked), above
+// it -max .. +infinity, above those NaN.
+struct Narrow {
+  typedef uint32_t T;
+  static constexpr T kNot = 0;
+  __device__ __forceinline__ static T of(float c) {
+    const uint32_t u = fbits(c + 0.0f);  // -0 is 0
+    return c != c ? ~0u : c == -__builtin_inff() ? 0u : u ^ (uint32_t)(((int32_t)u >> 31) | (int32_t)0x80000000);
   }
+  __device__ __forceinline__ static float logit(T k) {
+    return k == ~0u ? __builtin_nanf("") : k == 0 ? -__builtin_inff() : bitsf(k ^ (k >> 31 ? 0x80000000u : ~0u));
+  }
+  __device__ __forceinline__ static T max(T a, T b) { return a > b ? a : b; }
+  __device__ __forceinline__ static T min(T a, T b) { return a < b ? a : b; }
+  __device__ __forceinline__ static T sum(T a, T) { return a; }  // (pairs are never narrow)
+};
+// Choices as fp64 numbers: -infinity is not to be picked, NaN is +infinity and
+// +infinity the largest number (choices of fp32 biases are far below it).
+struct Wide {
+  typedef double T;
+  static constexpr T kNot = -__builtin_inf(), kMost = 1.7976931348623157e308;
+  // (the instructions themselves: the compiler's fmax first makes each operand that might be a signalling NaN a quiet one)
+  __device__ __forceinline__ static T max(T a, T b) {
+    asm("v_max_f64 %0, %1, %2" : "=v"(a) : "v"(a), "v"(b));
+    return a;
+  }
+  __device__ __forceinline__ static T min(T a, T b) {
+    asm("v_min_f64 %0, %1, %2" : "=v"(a) : "v"(a), "v"(b));
+    return a;
+  }
+  __device__ __forceinline__ static T of(double c) {
+    const double m = min(c, kMost);
+    return c != c ? __builtin_inf() : m;
+  }
+  __device__ __forceinline__ static T sum(T a, T b) {  // of a group's two largest, a >= b
+    return b == kNot ? a : a > kMost ? a : min(a + b, kMost);
+  }
+};
+
+// ---------------------------------------------------------------- across lanes
+
+// The two largest keys, of n lanes.
+template <class K>
+struct Two {
+  typename K::T a, b;
+  __device__ __forceinline__ void add(typename K::T k) {
+    b = K::max(b, K::min(a, k));
+    a = K::max(a, k);
+  }
+};
+// The value of another lane: DPP within a row of 16 lanes.
+template <int CTRL, typename T>
+__device__ __forceinline__ T dpp(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(T, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, 0xF, 0xF, true),
+                                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, 0xF, 0xF, true)});
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+  }
+}
+template <int CTRL, class K>
+__device__ __forceinline__ Two<K> dpp(Two<K> v) {
+  return {dpp<CTRL>(v.a), dpp<CTRL>(v.b)};
+}
+// f(1) .. f(15), as constants.
+template <typename F, int... I>
+__device__ __forceinline__ void unroll_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I + 1>{}), ...);
+}
+template <typename F>
+__device__ __forceinline__ void unroll16(F f) {
+  unroll_of(f, std::make_integer_sequence<int, 15>{});
+}
+// v and its counterpart of the other half of 32 (HALF = 16) or 64 (32) lanes, in both halves alike.
+template <int HALF, typename T>
+__device__ __forceinline__ void halves(T v, T& a, T& b) {
+  auto one = [](uint32_t x, uint32_t& p, uint32_t& q) {
+    const auto r = HALF == 16 ? __builtin_amdgcn_permlane16_swap(x, x, false, false) : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    p = r[0], q = r[1];
+  };
+  if constexpr (sizeof(T) == 8) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    uint32_t p[2], q[2];
+    one(u.x, p[0], q[0]);
+    one(u.y, p[1], q[1]);
+    a = __builtin_bit_cast(T, u32x2{p[0], p[1]});
+    b = __builtin_bit_cast(T, u32x2{q[0], q[1]});
+  } else {
+    uint32_t p, q;
+    one(__builtin_bit_cast(uint32_t, v), p, q);
+    a = __builtin_bit_cast(T, p);
+    b = __builtin_bit_cast(T, q);
+  }
+}
+template <int HALF, class K>
+__device__ __forceinline__ void halves(Two<K> v, Two<K>& a, Two<K>& b) {
+  halves<HALF>(v.a, a.a, b.a);
+  halves<HALF>(v.b, a.b, b.b);
+}
+// op over the n lanes (a power of two) that share lane / n, in all of them.
+template <typename T, typename F>
+__device__ __forceinline__ T over(T v, int n, F op) {
+  if (n > 1) v = op(v, dpp<0xB1>(v));   // lane ^ 1
+  if (n > 2) v = op(v, dpp<0x4E>(v));   // lane ^ 2
+  if (n > 4) v = op(v, dpp<0x141>(v));  // mirrored in 8
+  if (n > 8) v = op(v, dpp<0x140>(v));  // mirrored in 16
+  T a, b;
+  if (n > 16) halves<16>(v, a, b), v = op(a, b);
+  if (n > 32) halves<32>(v, a, b), v = op(a, b);
   return v;
+}
+template <class K>
+__device__ __forceinline__ typename K::T max_over(typename K::T v, int n) {
+  return over(v, n, [](auto a, auto b) { return K::max(a, b); });
 }
 template <typename T>
 __device__ __forceinline__ T sum_over(T v, int n) {
-  for (int d = 1; d < n; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  return over(v, n, [](T a, T b) { return a + b; });
 }
 
-// The two largest keys, and those of two such pairs.
-template <typename K>
-struct Two {
-  K a, b;
-  __device__ __forceinline__ void add(K k) {
-    b = k > a ? a : k > b ? k : b;
-    a = k > a ? k : a;
-  }
-};
-template <typename K>
-__device__ __forceinline__ Two<K> two_over(Two<K> t, int n) {
-  for (int d = 1; d < n; d <<= 1) {
-    const K oa = __shfl_xor(t.a, d), ob = __shfl_xor(t.b, d);
-    const K low = t.a > oa ? oa : t.a;
-    t.a = t.a > oa ? t.a : oa;
-    t.b = t.b > ob ? t.b : ob;
-    t.b = t.b > low ? t.b : low;
-  }
-  return t;
+template <class K>
+__device__ __forceinline__ typename K::T group_value(Two<K> t, int n, bool pairs) {
+  if (!pairs) return max_over<K>(t.a, n);
+  const Two<K> r = over(t, n, [](Two<K> x, Two<K> y) { return Two<K>{K::max(x.a, y.a), K::max(K::min(x.a, y.a), K::max(x.b, y.b))}; });
+  return K::sum(r.a, r.b);
 }
-template <typename K>
-__device__ __forceinline__ K group_value(Two<K> t, bool pairs) {
-  if (!pairs || t.b == 0) return t.a;
-  return key_of(value_of(t.a) + value_of(t.b));
+
+// ---------------------------------------------------------------- fp64 scores
+
+// exp(x), -800 <= x <= 800 (beyond fp64's range 0 and infinity): x = n ln 2 + r, |r| <= ln 2 / 2, ln 2 in two parts
+// (Cody and Waite's reduction), exp(r) by its series to r^12 / 12! (the rest is below 2^-52), times 2^n.  The library's
+// takes twice the instructions, and 16 scores a lane are most of this kernel's.
+__device__ __forceinline__ double exp64(double x) {
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, x));
+  // (the multiply-add as an instruction: the compiler's takes each constant into the result's registers first)
+  auto step = [&](double p, double k) {
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(p) : "v"(p), "v"(r), "s"(k));
+    return p;
+  };
+  double p = 1.0 / 479001600.0;
+  constexpr double c[] = {1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0,
+                          1.0 / 120.0,      1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+#pragma unroll
+  for (double k : c) p = step(p, k);
+  return __builtin_ldexp(p, (int)n);
+}
+// c ? a : b without a branch around what a takes.
+__device__ __forceinline__ double either(bool c, double a, double b) {
+  asm("" : "+v"(a));
+  asm("" : "+v"(b));
+  return c ? a : b;
+}
+// 1 / (1 + exp(-l)), NaN for NaN, 0 where exp(-l) leaves fp64's range.  The reciprocal is the hardware's with two
+// Newton steps.
+__device__ __forceinline__ double sigmoid64(float l) {
+  constexpr float far = -709.78265f;  // the last fp32 number above -1024 ln 2
+  const double d = 1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l, far, 800.0f));
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return either(l != l, __builtin_nan(""), either(l < far, 0.0, r));
+}
+// exp(l - peak): 0 for -infinity, NaN where either is NaN or the peak +infinity.
+__device__ __forceinline__ double below_peak64(float l, float peak) {
+  const double e = exp64(__builtin_fmax((double)l - (double)peak, -800.0));
+  return either(l == -__builtin_inff(), 0.0, either(l != l, __builtin_nan(""), e + ((double)peak - (double)peak)));
 }
 
 // ---------------------------------------------------------------- picking
 
 struct Layout {
   int q, lanes, per;  // experts of a lane, lanes of a group, experts of a group
-  bool loose;         // groups that do not fall on lanes
+  bool whole;         // every lane has a multiple of 4 experts
 };
 
 __device__ __forceinline__ float logit_at(const RouteArgs& a, int64_t m, int e) {
@@ -104,14 +219,70 @@ __device__ __forceinline__ int block_before(int v, int* total) {
   const int upto = wave_scan(v);
   if (lane == 63) total[wave] = upto;
   __syncthreads();
-  int before = upto - v;
-  for (int w = 0; w < wave; ++w) before += total[w];
-  return before;
+  const int waves = lane < wave ? total[lane & 15] : 0;  // (at most 16)
+  return upto - v + __builtin_amdgcn_readlane(wave_scan(waves), 63);
 }
 
-template <int L, int R, bool WIDE>
+// A choice on its way to the second launch: its expert and its rank among its
+// stretch's choices of that expert, -1 for none.  (Stretches have 2^22 tokens or
+// more only where M is 2^30 and so E too small for an expert's ten bits to be set.)
+constexpr int kRankBits = 22;
+
+// n <= R fp32 (or bf16) numbers from byte offset `at` on, `fill` past them.  No
+// branch but the uniform ones: each would wait for the loads before it.
+// `whole`: n is a multiple of 4 in every lane.
+template <int R>
+__device__ __forceinline__ void load_run(__amdgpu_buffer_rsrc_t from, uint32_t at, int n, bool half, bool whole, float fill, float* to) {
+  if (R >= 4 && whole) {
+    u32x4 w[(R + 3) / 4];
+#pragma unroll
+    for (int r = 0; r < R; r += 4) {
+      if (half) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(from, (int)(r < n ? at + 2 * r : kOut), 0, 0);
+        w[r / 4].x = v.x, w[r / 4].y = v.y;
+      } else {
+        w[r / 4] = bload128(from, r < n ? at + 4 * r : kOut);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const u32x4 v = w[r / 4];
+      const float wide = bitsf(v[r & 3]), narrow = bitsf(r & 1 ? v[(r & 3) >> 1] & 0xFFFF0000u : v[(r & 3) >> 1] << 16);
+      to[r] = r < n ? (half ? narrow : wide) : fill;
+    }
+  } else {
+    uint32_t w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = half ? bload16(from, r < n ? at + 2 * r : kOut) << 16 : bload32(from, r < n ? at + 4 * r : kOut);
+#pragma unroll
+    for (int r = 0; r < R; ++r) to[r] = r < n ? bitsf(w[r]) : fill;
+  }
+}
+
+// Groups before this lane's: of a larger value, or an equal one and a lower index.
+template <int L, class K>
+__device__ __forceinline__ int better_groups(typename K::T v, int group, int lanes, int groups, int lane) {
+  int better = 0;
+  if constexpr (L == 16) {
+    unroll16([&](auto by) {  // the values of lanes by, by ... further, round the row
+      constexpr int BY = decltype(by)::value;
+      if (BY % lanes) return;  // (uniform)
+      const typename K::T o = dpp<0x120 + BY>(v);
+      better += o > v || (o == v && dpp<0x120 + BY>(group) < group);
+    });
+  } else {
+    for (int g = 0; g < groups; ++g) {
+      const typename K::T o = __shfl(v, lane / L * L + g * lanes);
+      better += o > v || (o == v && g < group);
+    }
+  }
+  return better;
+}
+
+template <int L, int R, class K, bool LOOSE>
 __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int passes) {
-  using K = std::conditional_t<WIDE, uint64_t, uint32_t>;
+  typedef typename K::T T;
+  constexpr bool WIDE = sizeof(T) == 8;
   constexpr int AT_ONCE = kThreads / L;  // tokens
   static_assert(kPassTokens % AT_ONCE == 0, "whole rounds of a pass");
   __shared__ uint64_t mask[WQ_MAX_EXPERTS];
@@ -129,79 +300,84 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
   const int in_group = l % at.lanes, group = l / at.lanes;
   const int first = group * at.per + in_group * at.q;
   const int mine = max(0, min(at.q, min(at.per - in_group * at.q, E - first)));
-  const uint64_t seg = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << ((tid & 63) / L * L);
+  float bias[WIDE ? R : 1];
+  if constexpr (WIDE)
+    load_run<R>(make_rsrc(a.bias, a.bias ? (uint32_t)E * 4u : 0u), (uint32_t)first * 4u, mine, false, at.whole, -__builtin_inff(), bias);
 
   for (int pass = 0; pass < passes; ++pass) {
     const int64_t m0 = ((int64_t)blockIdx.x * passes + pass) * kPassTokens;
-    for (int sub = 0; sub < kPassTokens; sub += AT_ONCE) {
+    if (m0 >= a.M) break;
+    const int tokens = (int)min((int64_t)kPassTokens, (int64_t)a.M - m0);
+    const __amdgpu_buffer_rsrc_t rows = make_rsrc(static_cast<const char*>(a.logits) + m0 * a.ld * (a.half ? 2 : 4),
+                                                  ((uint32_t)(tokens - 1) * (uint32_t)a.ld + (uint32_t)E) * (a.half ? 2u : 4u));
+    for (int sub = 0; sub < kPassTokens && m0 + sub < a.M; sub += AT_ONCE) {
       const int t = sub + slot;
       const int64_t m = m0 + t;
       const bool live = m < a.M && (!a.valid || a.valid[m]);
-      K key[R];
+      T key[R];
       uint32_t biggest = 0;  // key of the row's largest logit
-      float logit[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        logit[r] = live && r < mine ? logit_at(a, m, first + r) : -__builtin_inff();
-        biggest = max(biggest, key_of(logit[r]));
-      }
-      biggest = max_over(biggest, L);
-      const float peak = value_of(biggest);
       double sum = 0.0;
-      if constexpr (WIDE) {
-        double s[R];
+      float peak;
+      {
+        float logit[R];
+        load_run<R>(rows, ((uint32_t)t * (uint32_t)a.ld + (uint32_t)first) * (a.half ? 2u : 4u), live ? mine : 0, a.half, at.whole,
+                    -__builtin_inff(), logit);
+        if (!a.sigmoid || !WIDE) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const bool on = logit[r] != -__builtin_inff();
-          if (a.sigmoid) {
-            s[r] = 1.0 / (1.0 + exp(-(double)logit[r]));
-          } else {
-            s[r] = on ? exp((double)logit[r] - (double)peak) : 0.0;
-            sum += s[r];
+          for (int r = 0; r < R; ++r) {
+            const uint32_t k = Narrow::of(logit[r]);
+            if constexpr (!WIDE) key[r] = k;
+            biggest = max(biggest, k);
           }
+          biggest = max_over<Narrow>(biggest, L);
         }
-        if (!a.sigmoid) {
-          sum = sum_over(sum, L);
+        peak = Narrow::logit(biggest);
+        if constexpr (WIDE) {
+          double part = 1.0;
+          if (a.sigmoid) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) s[r] /= sum;
+            for (int r = 0; r < R; ++r) {
+              key[r] = sigmoid64(logit[r]);
+              if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (16 at once would not fit the registers)
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              sum += key[r] = below_peak64(logit[r], peak);
+              if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+            sum = sum_over(sum, L);
+            part = 1.0 / sum;
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) key[r] = either(logit[r] == -__builtin_inff(), K::kNot, K::of(key[r] * part + (double)bias[r]));
+        } else if (!a.sigmoid && !a.renormalize) {
+          float each = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) each += logit[r] == -__builtin_inff() ? 0.f : expf(logit[r] - peak);
+          sum = sum_over(each, L);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          key[r] = r < mine && logit[r] != -__builtin_inff() ? key_of(s[r] + (a.bias ? (double)a.bias[first + r] : 0.0)) : 0;
-      } else {
-        float part = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          key[r] = key_of(logit[r]);
-          if (!a.sigmoid && !a.renormalize) part += logit[r] == -__builtin_inff() ? 0.f : expf(logit[r] - peak);
-        }
-        sum = sum_over(part, L);
       }
 
       if (a.groups > 1) {
-        Two<K> two{0, 0};
-        if (!at.loose) {
+        if constexpr (!LOOSE) {
+          Two<K> two{K::kNot, K::kNot};
 #pragma unroll
           for (int r = 0; r < R; ++r) two.add(key[r]);
-          const K v = group_value(two_over(two, at.lanes), a.pairs);
-          int better = 0;
-          for (int g = 0; g < a.groups; ++g) {
-            const K o = __shfl(v, (tid & 63) / L * L + g * at.lanes);
-            better += o > v || (o == v && g < group);
-          }
-          if (better >= a.keep) {
+          const T v = group_value<K>(two, at.lanes, a.pairs);
+          if (better_groups<L, K>(v, group, at.lanes, a.groups, tid & 63) >= a.keep) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) key[r] = 0;
+            for (int r = 0; r < R; ++r) key[r] = K::kNot;
           }
         } else {
-          K* value = reinterpret_cast<K*>(loose) + slot * a.groups;
+          T* value = reinterpret_cast<T*>(loose) + slot * a.groups;
           const int size = E / a.groups;
           for (int g = 0; g < a.groups; ++g) {
-            Two<K> t2{0, 0};
+            Two<K> t2{K::kNot, K::kNot};
 #pragma unroll
             for (int r = 0; r < R; ++r)
               if ((first + r) / size == g) t2.add(key[r]);
-            const K v = group_value(two_over(t2, L), a.pairs);
+            const T v = group_value<K>(t2, L, a.pairs);
             if (l == 0) value[g] = v;
           }
           __syncthreads();
@@ -209,39 +385,37 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
           for (int r = 0; r < R; ++r) {
             if (r >= mine) continue;
             const int own = (first + r) / size;
-            const K v = value[own];
+            const T v = value[own];
             int better = 0;
             for (int g = 0; g < a.groups; ++g) better += value[g] > v || (value[g] == v && g < own);
-            if (better >= a.keep) key[r] = 0;
+            if (better >= a.keep) key[r] = K::kNot;
           }
           __syncthreads();
         }
       }
 
       int pick = -1;  // of lane j: the j-th largest choice
+      float x = 0.f;  // its logit
       for (int j = 0; j < top; ++j) {
-        K best = 0;
-        int br = 0;
+        T best = key[0];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (key[r] > best) best = key[r], br = r;
-        const K all = max_over(best, L);
-        const uint64_t holders = __ballot(best == all) & seg;
-        const int winner = __builtin_ctzll(holders);
-        const int e = __shfl(first + br, winner);
-        if (l == j && all != 0) pick = e;
-        if ((tid & 63) == winner) {
+        for (int r = 1; r < R; ++r) best = K::max(best, key[r]);
+        best = max_over<K>(best, L);
+        uint32_t e = ~0u;  // the lowest expert of that key
 #pragma unroll
-          for (int r = 0; r < R; ++r) key[r] = r == br ? 0 : key[r];
+        for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(first + r) : e;
+        e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+        if (l == j && best != K::kNot) {
+          pick = (int)e;
+          if constexpr (!WIDE) x = Narrow::logit(best);
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r) key[r] = (uint32_t)(first + r) == e ? K::kNot : key[r];
       }
+      if (WIDE && pick >= 0) x = logit_at(a, m, pick);
 
       double s = 0.0;
-      if (pick >= 0) {
-        const double x = logit_at(a, m, pick);
-        // (a peak of +infinity makes every score NaN, those of finite logits too)
-        s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)peak) + ((double)peak - (double)peak);
-      }
+      if (pick >= 0) s = a.sigmoid ? sigmoid64(x) : below_peak64(x, peak);
       if (a.renormalize) {
         const double all = sum_over(s, L);
         s = all == 0.0 ? 0.0 : s / all;
@@ -278,8 +452,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
       if (e != kNone) {
         p = base[e] + __builtin_popcountll(mask[e] & ((1ull << t) - 1));
         if (alone) a.rows[p] = t;
+        else p |= e << kRankBits;
       }
-      a.places[m0 * top + i] = p;  // (more than one stretch: the rank within this one)
+      a.places[m0 * top + i] = p;
     }
     if (!alone) {
       __syncthreads();
@@ -299,15 +474,25 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
 __global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passes) {
   __shared__ int before[WQ_MAX_EXPERTS], all[WQ_MAX_EXPERTS], total[kThreads / 64];
   const int tid = threadIdx.x, E = a.E, top = a.top, n = gridDim.x, b = blockIdx.x;
+  const int64_t m0 = (int64_t)b * passes * kPassTokens;
+  const int choices = (int)min((int64_t)passes * kPassTokens, (int64_t)a.M - m0) * top;
+  int32_t* places = a.places + m0 * top;
+  int next = tid < choices ? places[tid] : -1;  // (under way with the counts)
   for (int e = tid; e < E; e += kThreads) before[e] = 0, all[e] = 0;
   __syncthreads();
   const int wide = (E + 63) / 64 * 64, slices = kThreads / wide, slice = tid / wide, e = tid % wide;
   if (slice < slices && e < E) {
     int x = 0, y = 0;
-    for (int i = slice; i < n; i += slices) {
-      const int c = a.counts[(int64_t)i * E + e];
-      y += c;
-      x += i < b ? c : 0;
+    constexpr int AHEAD = 32;  // loads under way
+    for (int i = slice; i < n; i += AHEAD * slices) {
+      int c[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) c[u] = i + u * slices < n ? a.counts[(int64_t)(i + u * slices) * E + e] : 0;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        y += c[u];
+        x += i + u * slices < b ? c[u] : 0;
+      }
     }
     atomicAdd(&before[e], x);
     atomicAdd(&all[e], y);
@@ -323,21 +508,22 @@ __global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passe
     }
   }
   __syncthreads();
-  const int64_t m0 = (int64_t)b * passes * kPassTokens;
-  const int tokens = (int)min((int64_t)passes * kPassTokens, (int64_t)a.M - m0);
-  for (int i = tid; i < tokens * top; i += kThreads) {
-    const int pick = a.ids[m0 * top + i];
-    if (pick < 0) continue;
-    const int p = before[pick] + a.places[m0 * top + i];
-    a.places[m0 * top + i] = p;
-    a.rows[p] = (int32_t)(m0 + i / top);
+  for (int i = tid; i < choices;) {
+    const int c = next, at = i;
+    i += kThreads;
+    next = i < choices ? places[i] : -1;
+    if (c == -1) continue;
+    const int p = before[(uint32_t)c >> kRankBits] + (c & ((1 << kRankBits) - 1));
+    places[at] = p;
+    a.rows[p] = (int32_t)(m0 + at / top);
   }
 }
 
-template <int L, int R>
+template <int L, int R, bool LOOSE = false>
 hipError_t route_launch(const RouteArgs& a, const Layout& at, const Stretches& st, bool wide, hipStream_t s) {
-  const size_t smem = at.loose ? (size_t)(kThreads / L) * a.groups * (wide ? 8 : 4) : 0;
-  return launch(wide ? k_route<L, R, true> : k_route<L, R, false>, dim3((unsigned)st.count), kThreads, smem, s, a, at, st.passes);
+  const size_t smem = LOOSE ? (size_t)(kThreads / L) * a.groups * (wide ? 8 : 4) : 0;
+  return launch(wide ? k_route<L, R, Wide, LOOSE> : k_route<L, R, Narrow, LOOSE>, dim3((unsigned)st.count), kThreads, smem, s, a, at,
+                st.passes);
 }
 
 __global__ void k_no_tokens(int32_t* offsets, int n) {
@@ -355,15 +541,20 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   auto fits = [&](int lanes, int regs, Layout& at) {
     if (a.top > lanes || (on_lanes && a.groups > lanes)) return false;
     const int groups = on_lanes ? a.groups : 1;
-    at.loose = !on_lanes;
     at.per = a.E / groups;
     at.lanes = lanes / groups;
     at.q = (at.per + at.lanes - 1) / at.lanes;
+    at.whole = at.q % 4 == 0 && at.per % 4 == 0;
     return at.q <= regs;
   };
   Layout at;
-  hipError_t e;
-  if (fits(16, 1, at)) e = route_launch<16, 1>(a, at, st, wide, s);
+  hipError_t e = hipErrorInvalidValue;
+  const bool few = a.M <= kThreads / 64;
+  if (!on_lanes) e = fits(64, 4, at) ? route_launch<64, 4, true>(a, at, st, wide, s) : fits(64, 16, at) ? route_launch<64, 16, true>(a, at, st, wide, s) : e;
+  else if (few && fits(64, 1, at)) e = route_launch<64, 1>(a, at, st, wide, s);
+  else if (few && fits(64, 2, at)) e = route_launch<64, 2>(a, at, st, wide, s);
+  else if (few && fits(64, 4, at)) e = route_launch<64, 4>(a, at, st, wide, s);
+  else if (fits(16, 1, at)) e = route_launch<16, 1>(a, at, st, wide, s);
   else if (fits(16, 2, at)) e = route_launch<16, 2>(a, at, st, wide, s);
   else if (fits(16, 4, at)) e = route_launch<16, 4>(a, at, st, wide, s);
   else if (fits(16, 8, at)) e = route_launch<16, 8>(a, at, st, wide, s);
@@ -372,7 +563,6 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   else if (fits(32, 16, at)) e = route_launch<32, 16>(a, at, st, wide, s);
   else if (fits(64, 4, at)) e = route_launch<64, 4>(a, at, st, wide, s);
   else if (fits(64, 16, at)) e = route_launch<64, 16>(a, at, st, wide, s);
-  else return hipErrorInvalidValue;
   if (e != hipSuccess || (st.count == 1 && st.passes == 1)) return e;
   return launch(k_route_order, dim3((unsigned)st.count), kThreads, 0, s, a, st.passes);
 }
