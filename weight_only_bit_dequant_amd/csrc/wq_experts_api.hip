@@ -12,7 +12,7 @@ extern "C" {
 
 size_t wq_experts_route_workspace(int64_t M, int64_t E) {
   if (M <= wq::kPassTokens || E <= 0 || M > kMaxDim || E > WQ_MAX_EXPERTS) return 0;
-  return (size_t)wq::stretches(M).count * (size_t)E * sizeof(int32_t);
+  return (size_t)wq::stretches(M).count * (size_t)wq::counts_pitch((int)E) * sizeof(uint16_t);
 }
 
 wq_status wq_experts_route(const void* logits, int logit_bits, int64_t ld, int64_t M, int64_t E, int64_t top, int score,
@@ -54,7 +54,7 @@ wq_status wq_experts_route(const void* logits, int logit_bits, int64_t ld, int64
   a.offsets = offsets;
   a.rows = rows;
   a.places = places;
-  a.counts = (int32_t*)workspace;
+  a.counts = (uint16_t*)workspace;
   a.M = (int)M;
   a.E = (int)E;
   a.top = (int)top;

@@ -3,6 +3,8 @@
 // arguments were validated by the ABI layer.
 #pragma once
 
+#include <hip/hip_runtime.h>
+
 #include "wq_block_internal.hpp"
 #include "wq_experts.h"
 
@@ -18,22 +20,25 @@ struct RouteArgs {
   int32_t* offsets;
   int32_t* rows;
   int32_t* places;
-  int32_t* counts;  // workspace: choices of each stretch of tokens by expert
+  uint16_t* counts;  // workspace: choices of each stretch of tokens by expert
   int M, E, top, groups, keep;
   float scale;
   bool half, sigmoid, pairs, renormalize;
 };
 
-// Tokens in stretches, one to a workgroup: `passes` times kPassTokens each.
-constexpr int kPassTokens = 64, kMaxStretches = 256;
+// Tokens in stretches, one to a workgroup: `passes` times kPassTokens each, at
+// most 2^16 - 64 (a stretch's counts have 16 bits).
+constexpr int kPassTokens = 64, kMaxStretches = 256, kMaxPasses = 1023;
 struct Stretches {
   int passes, count;
 };
 inline Stretches stretches(int64_t M) {
-  const int64_t all = (M + kPassTokens - 1) / kPassTokens;
-  const int64_t passes = all ? (all + kMaxStretches - 1) / kMaxStretches : 1;
+  const int64_t all = (M + kPassTokens - 1) / kPassTokens, even = (all + kMaxStretches - 1) / kMaxStretches;
+  const int64_t passes = even < 1 ? 1 : even < kMaxPasses ? even : kMaxPasses;
   return {(int)passes, (int)((all + passes - 1) / passes)};
 }
+// Counts of a stretch, whole words.
+inline __host__ __device__ int counts_pitch(int E) { return (E + 1) & ~1; }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 

@@ -224,9 +224,8 @@ __device__ __forceinline__ int block_before(int v, int* total) {
 }
 
 // A choice on its way to the second launch: its expert and its rank among its
-// stretch's choices of that expert, -1 for none.  (Stretches have 2^22 tokens or
-// more only where M is 2^30 and so E too small for an expert's ten bits to be set.)
-constexpr int kRankBits = 22;
+// stretch's choices of that expert, -1 for none.
+constexpr int kRankBits = 16;
 
 // n <= R fp32 (or bf16) numbers from byte offset `at` on, `fill` past them.  No
 // branch but the uniform ones: each would wait for the loads before it.
@@ -466,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
     }
   }
   if (!alone)
-    for (int e = tid; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * E + e] = base[e];
+    for (int e = tid; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * counts_pitch(E) + e] = (uint16_t)base[e];
 }
 
 // ---------------------------------------------------------------- the order of many stretches
@@ -480,22 +479,30 @@ __global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passe
   int next = tid < choices ? places[tid] : -1;  // (under way with the counts)
   for (int e = tid; e < E; e += kThreads) before[e] = 0, all[e] = 0;
   __syncthreads();
-  const int wide = (E + 63) / 64 * 64, slices = kThreads / wide, slice = tid / wide, e = tid % wide;
-  if (slice < slices && e < E) {
-    int x = 0, y = 0;
-    constexpr int AHEAD = 32;  // loads under way
+  // two experts to a thread, so that few loads, all under way at once, take a stretch's counts
+  const int words = counts_pitch(E) / 2, wide = (words + 63) / 64 * 64, slices = kThreads / wide, slice = tid / wide, w = tid % wide;
+  if (slice < slices && w < words) {
+    int x[2] = {0, 0}, y[2] = {0, 0};
+    constexpr int AHEAD = 32;
+    const uint32_t* counts = reinterpret_cast<const uint32_t*>(a.counts) + w;
     for (int i = slice; i < n; i += AHEAD * slices) {
-      int c[AHEAD];
+      uint32_t c[AHEAD];
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) c[u] = i + u * slices < n ? a.counts[(int64_t)(i + u * slices) * E + e] : 0;
+      for (int u = 0; u < AHEAD; ++u) c[u] = i + u * slices < n ? counts[(int64_t)(i + u * slices) * words] : 0;
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
-        y += c[u];
-        x += i + u * slices < b ? c[u] : 0;
+        const int lo = (int)(c[u] & 0xFFFFu), hi = (int)(c[u] >> 16);
+        const bool earlier = i + u * slices < b;
+        y[0] += lo, y[1] += hi;
+        x[0] += earlier ? lo : 0, x[1] += earlier ? hi : 0;
       }
     }
-    atomicAdd(&before[e], x);
-    atomicAdd(&all[e], y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (2 * w + k < E) {
+        atomicAdd(&before[2 * w + k], x[k]);
+        atomicAdd(&all[2 * w + k], y[k]);
+      }
   }
   __syncthreads();
   const int mine = tid < E ? all[tid] : 0;

@@ -53,16 +53,24 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   return r;
 }
 
-// Codes of y / s, the quotient as y * (1 / s) and one correction by its
+// Codes of y / s.  EXACT: the quotient as y * (1 / s) and one correction by its
 // remainder: IEEE division's result but for rare last bits, at a third of its
-// instructions.  |y / s| < 127.5 by the choice of s.  Adding 1.5 * 2^23 rounds
-// to a whole number, ties to even, whose low byte is the sum's.
+// instructions.  (Of bf16 rows a thousandth of the quotients are within an ulp of a
+// tie: y * (1 / s) alone takes two in three of those to the other side.)  Otherwise,
+// where y itself was rounded, the product.  Adding 1.5 * 2^23 rounds to a whole
+// number, ties to even, whose low byte is the sum's.  |y / s| < 127.5 by the choice
+// of s.
+template <bool EXACT>
 __device__ __forceinline__ u32x2 codes8(const F8& y, const RowScale& r) {
   uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = y.v[i] * r.inv;
-    b[i] = fbits(__builtin_fmaf(__builtin_fmaf(-v, r.s, y.v[i]), r.inv, v) + 12582912.0f);
+    if constexpr (EXACT) {
+      const float v = y.v[i] * r.inv;
+      b[i] = fbits(__builtin_fmaf(__builtin_fmaf(-v, r.s, y.v[i]), r.inv, v) + 12582912.0f);
+    } else {
+      b[i] = fbits(__builtin_fmaf(y.v[i], r.inv, 12582912.0f));
+    }
   }
   u32x2 w;
 #pragma unroll
@@ -72,6 +80,17 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, const RowScale& r) {
     w[h] = r.bad ? 0u : lo | hi;
   }
   return w;
+}
+
+// silu(g) u = g / (1 + exp(-g)) u on the hardware's 2^x and reciprocal (an ulp
+// each).  The exponent's one rounding makes exp(-g) off by |g| 2^-24 of itself: what
+// counts of that is below 2^-21 where silu is more than a millionth of its size
+// elsewhere, far below a code's step.  Where exp(-g) passes 2^126 (g < -87.3) the
+// result is -0; infinities and NaN are as the formula has them.  Six instructions; one
+// more exact by two bits takes sixteen and is this kernel's time (4096 x 5632: 30 us).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float d = 1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f);
+  return g * __builtin_amdgcn_rcpf(d) * u;
 }
 
 __device__ __forceinline__ float stored(const RowScale& r) { return r.bad ? __builtin_nanf("") : r.s; }
@@ -115,7 +134,7 @@ __global__ __launch_bounds__(rows_per_group<WPR>() * WPR * 64) void k_int8_rows(
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     const uint32_t c = c0 + 64u * WPR * j;
-    if (live && c * 8u < (uint32_t)K) *reinterpret_cast<u32x2*>(Xq + m * K + c * 8u) = codes8(y[j], r);
+    if (live && c * 8u < (uint32_t)K) *reinterpret_cast<u32x2*>(Xq + m * K + c * 8u) = codes8<!GATE>(y[j], r);
   }
   if (live && c0 == 0) Xs[m] = stored(r);
 }
@@ -140,7 +159,7 @@ __global__ __launch_bounds__(1024) void k_int8_long_rows(const uint16_t* X, int6
   uint32_t amax = 0;
   for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) amax = max(amax, absmax8(at(k)));
   const RowScale r = row_scale(row_max<16>(amax, part, wave, lane));
-  for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) *reinterpret_cast<u32x2*>(Xq + m * K + k) = codes8(at(k), r);
+  for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) *reinterpret_cast<u32x2*>(Xq + m * K + k) = codes8<!GATE>(at(k), r);
   if (threadIdx.x == 0) Xs[m] = stored(r);
 }
 
