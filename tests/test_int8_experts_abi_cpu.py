@@ -152,7 +152,7 @@ def test_route():
     assert route(M=1 << 29) == wq.EUNSUPPORTED
     assert route(M=1 << 62) == wq.EUNSUPPORTED
     need = experts._lib().wq_experts_route_workspace(65, 12)
-    assert need == 2 * 12 * 2
+    assert need == 5 * 12 * 2
     assert route(M=65) == wq.EWORKSPACE
     assert route(M=65, WS=4, ws=need - 1) == wq.EWORKSPACE
     assert route(M=65, WS=2, ws=need) == wq.EALIGN
@@ -160,7 +160,7 @@ def test_route():
 
 def test_route_workspace():
     size = experts._lib().wq_experts_route_workspace
-    assert size(0, 8) == size(-5, 8) == size(64, 8) == size(1000, 0) == size(1000, 2000) == size(1 << 40, 8) == 0
+    assert size(0, 8) == size(-5, 8) == size(16, 8) == size(1000, 0) == size(1000, 2000) == size(1 << 40, 8) == 0
     assert size(64 * 256, 8) == 256 * 8 * 2
     for M in (65, 1000, 16384, 16385, 100000, 1 << 24):
         assert 0 < size(M, 1024) <= 257 * 1024 * 2

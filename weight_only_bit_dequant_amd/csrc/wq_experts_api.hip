@@ -11,7 +11,7 @@ using namespace wq::api;
 extern "C" {
 
 size_t wq_experts_route_workspace(int64_t M, int64_t E) {
-  if (M <= wq::kPassTokens || E <= 0 || M > kMaxDim || E > WQ_MAX_EXPERTS) return 0;
+  if (M <= wq::kFewSpan || E <= 0 || M > kMaxDim || E > WQ_MAX_EXPERTS) return 0;
   return (size_t)wq::stretches(M).count * (size_t)wq::counts_pitch((int)E) * sizeof(uint16_t);
 }
 

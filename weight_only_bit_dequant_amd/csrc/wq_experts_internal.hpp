@@ -26,16 +26,18 @@ struct RouteArgs {
   bool half, sigmoid, pairs, renormalize;
 };
 
-// Tokens in stretches, one to a workgroup: `passes` times kPassTokens each, at
-// most 2^16 - 64 (a stretch's counts have 16 bits).
-constexpr int kPassTokens = 64, kMaxStretches = 256, kMaxPasses = 1023;
+// Tokens in stretches, one to a workgroup: `passes` times `span` tokens each, at
+// most 2^16 - 64 in all (a stretch's counts have 16 bits).  Few tokens are spread
+// over the chip, a wave to each; many share a wave.
+constexpr int kFewSpan = 16, kSpan = 64, kMaxStretches = 256, kMaxPasses = 1023;
 struct Stretches {
-  int passes, count;
+  int span, passes, count;
 };
 inline Stretches stretches(int64_t M) {
-  const int64_t all = (M + kPassTokens - 1) / kPassTokens, even = (all + kMaxStretches - 1) / kMaxStretches;
-  const int64_t passes = even < 1 ? 1 : even < kMaxPasses ? even : kMaxPasses;
-  return {(int)passes, (int)((all + passes - 1) / passes)};
+  if (M <= kFewSpan * kMaxStretches) return {kFewSpan, 1, M ? (int)((M + kFewSpan - 1) / kFewSpan) : 1};
+  const int64_t all = (M + kSpan - 1) / kSpan, even = (all + kMaxStretches - 1) / kMaxStretches;
+  const int64_t passes = even < kMaxPasses ? even : kMaxPasses;
+  return {kSpan, (int)passes, (int)((all + passes - 1) / passes)};
 }
 // Counts of a stretch, whole words.
 inline __host__ __device__ int counts_pitch(int E) { return (E + 1) & ~1; }

@@ -10,12 +10,17 @@
 // that choices next to each other are in the order of the definition (an fp32
 // score is off by 2^-24, and one token in some thousand has choices that near).
 //
-// The order needs no atomics whose order counts: of each kPassTokens tokens a bit
-// mask of those that picked an expert gives every choice its rank among them
-// (the bits below its own) and the expert its count.  Up to kPassTokens tokens
-// take one launch of one workgroup; more take two: the first writes counts of
-// each stretch of tokens, in the second each workgroup adds up the counts before
-// its own.
+// The order needs no atomics whose order counts: of each `span` tokens a bit mask
+// of those that picked an expert gives every choice its rank among them (the bits
+// below its own) and the expert its count.  A few tokens take one launch of one
+// workgroup; more take two: the first writes counts of each stretch of tokens, in
+// the second each workgroup adds up the counts before its own.
+//
+// What bounds it: 16384 tokens of 256 experts (sigmoid, bias, the best 4 of 8 groups)
+// take 24 us in the first launch, instructions: of some 1900 for four tokens half are
+// the eight picks, a quarter the scores in fp64.  The second takes 7 us, a few trips to
+// memory.  By the logits alone the first takes 11 us.  One token takes 4.9 us, 2.5 of
+// them the launch, one trip to memory, and the picks one after the other.
 #include <type_traits>
 #include <utility>
 
@@ -26,7 +31,7 @@ namespace wq {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kOrderThreads = 512;
 constexpr uint16_t kNone = 0xFFFF;
 
 // ---------------------------------------------------------------- keys
@@ -104,6 +109,15 @@ __device__ __forceinline__ void unroll_of(F f, std::integer_sequence<int, I...>)
 template <typename F>
 __device__ __forceinline__ void unroll16(F f) {
   unroll_of(f, std::make_integer_sequence<int, 15>{});
+}
+template <typename T>
+__device__ __forceinline__ T read_lane(T v, int lane) {
+  if constexpr (sizeof(T) == 8) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(T, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)u.x, lane), (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)});
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  }
 }
 // v and its counterpart of the other half of 32 (HALF = 16) or 64 (32) lanes, in both halves alike.
 template <int HALF, typename T>
@@ -271,28 +285,29 @@ __device__ __forceinline__ int better_groups(typename K::T v, int group, int lan
     });
   } else {
     for (int g = 0; g < groups; ++g) {
-      const typename K::T o = __shfl(v, lane / L * L + g * lanes);
+      typename K::T o;
+      if constexpr (L == 64) o = read_lane(v, g * lanes);
+      else o = __shfl(v, lane / L * L + g * lanes);
       better += o > v || (o == v && g < group);
     }
   }
   return better;
 }
 
-template <int L, int R, class K, bool LOOSE>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int passes) {
+template <int L, int R, class K, bool LOOSE, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int span, int passes) {
   typedef typename K::T T;
   constexpr bool WIDE = sizeof(T) == 8;
-  constexpr int AT_ONCE = kThreads / L;  // tokens
-  static_assert(kPassTokens % AT_ONCE == 0, "whole rounds of a pass");
+  constexpr int AT_ONCE = THREADS / L;  // tokens
   __shared__ uint64_t mask[WQ_MAX_EXPERTS];
   __shared__ int base[WQ_MAX_EXPERTS];
-  __shared__ uint16_t picks[kPassTokens * WQ_MAX_TOP];
-  __shared__ int total[kThreads / 64];
+  __shared__ uint16_t picks[kSpan * WQ_MAX_TOP];
+  __shared__ int total[THREADS / 64];
   extern __shared__ __attribute__((aligned(16))) unsigned char loose[];  // keys of loose groups: [AT_ONCE][groups]
   const int tid = threadIdx.x, l = tid % L, slot = tid / L;
   const int E = a.E, top = a.top;
   const bool alone = gridDim.x == 1 && passes == 1;  // this workgroup has all tokens
-  for (int e = tid; e < E; e += kThreads) mask[e] = 0, base[e] = 0;
+  for (int e = tid; e < E; e += THREADS) mask[e] = 0, base[e] = 0;
   __syncthreads();
 
   // this lane's experts: first .. first + mine - 1
@@ -304,12 +319,12 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
     load_run<R>(make_rsrc(a.bias, a.bias ? (uint32_t)E * 4u : 0u), (uint32_t)first * 4u, mine, false, at.whole, -__builtin_inff(), bias);
 
   for (int pass = 0; pass < passes; ++pass) {
-    const int64_t m0 = ((int64_t)blockIdx.x * passes + pass) * kPassTokens;
+    const int64_t m0 = ((int64_t)blockIdx.x * passes + pass) * span;
     if (m0 >= a.M) break;
-    const int tokens = (int)min((int64_t)kPassTokens, (int64_t)a.M - m0);
+    const int tokens = (int)min((int64_t)span, (int64_t)a.M - m0);
     const __amdgpu_buffer_rsrc_t rows = make_rsrc(static_cast<const char*>(a.logits) + m0 * a.ld * (a.half ? 2 : 4),
                                                   ((uint32_t)(tokens - 1) * (uint32_t)a.ld + (uint32_t)E) * (a.half ? 2u : 4u));
-    for (int sub = 0; sub < kPassTokens && m0 + sub < a.M; sub += AT_ONCE) {
+    for (int sub = 0; sub < tokens; sub += AT_ONCE) {
       const int t = sub + slot;
       const int64_t m = m0 + t;
       const bool live = m < a.M && (!a.valid || a.valid[m]);
@@ -403,7 +418,11 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
         uint32_t e = ~0u;  // the lowest expert of that key
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(first + r) : e;
-        e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+        if constexpr (L == 64) {
+          e = __builtin_amdgcn_readlane(e, __builtin_ctzll(__ballot(e != ~0u)));
+        } else {
+          e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+        }
         if (l == j && best != K::kNot) {
           pick = (int)e;
           if constexpr (!WIDE) x = Narrow::logit(best);
@@ -433,19 +452,30 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
     __syncthreads();
 
     if (alone) {
-      // offsets, then places and rows at once
-      const int n = tid < E ? __builtin_popcountll(mask[tid]) : 0;
-      const int before = block_before(n, total);
-      if (tid < E) {
-        base[tid] = before;
-        a.offsets[tid] = before;
-        if (tid == E - 1) a.offsets[E] = before + n;
+      // offsets, then places and rows at once; a thread has PER experts
+      constexpr int PER = WQ_MAX_EXPERTS / THREADS;
+      int n[PER], sum = 0;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int e = tid * PER + u;
+        n[u] = e < E ? __builtin_popcountll(mask[e]) : 0;
+        sum += n[u];
+      }
+      int before = block_before(sum, total);
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int e = tid * PER + u;
+        if (e < E) {
+          base[e] = before;
+          a.offsets[e] = before;
+          before += n[u];
+          if (e == E - 1) a.offsets[E] = before;
+        }
       }
       __syncthreads();
     }
-    for (int i = tid; i < kPassTokens * top; i += kThreads) {
+    for (int i = tid; i < tokens * top; i += THREADS) {
       const int t = i / top;
-      if (m0 + t >= a.M) break;
       const int e = picks[i];
       int p = -1;
       if (e != kNone) {
@@ -457,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
     }
     if (!alone) {
       __syncthreads();
-      for (int e = tid; e < E; e += kThreads) {
+      for (int e = tid; e < E; e += THREADS) {
         base[e] += __builtin_popcountll(mask[e]);
         mask[e] = 0;
       }
@@ -465,22 +495,22 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, Layout at, int 
     }
   }
   if (!alone)
-    for (int e = tid; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * counts_pitch(E) + e] = (uint16_t)base[e];
+    for (int e = tid; e < E; e += THREADS) a.counts[(int64_t)blockIdx.x * counts_pitch(E) + e] = (uint16_t)base[e];
 }
 
 // ---------------------------------------------------------------- the order of many stretches
 
-__global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passes) {
-  __shared__ int before[WQ_MAX_EXPERTS], all[WQ_MAX_EXPERTS], total[kThreads / 64];
+__global__ __launch_bounds__(kOrderThreads) void k_route_order(RouteArgs a, int tokens) {
+  __shared__ int before[WQ_MAX_EXPERTS], all[WQ_MAX_EXPERTS], total[kOrderThreads / 64];
   const int tid = threadIdx.x, E = a.E, top = a.top, n = gridDim.x, b = blockIdx.x;
-  const int64_t m0 = (int64_t)b * passes * kPassTokens;
-  const int choices = (int)min((int64_t)passes * kPassTokens, (int64_t)a.M - m0) * top;
+  const int64_t m0 = (int64_t)b * tokens;
+  const int choices = (int)min((int64_t)tokens, (int64_t)a.M - m0) * top;
   int32_t* places = a.places + m0 * top;
   int next = tid < choices ? places[tid] : -1;  // (under way with the counts)
-  for (int e = tid; e < E; e += kThreads) before[e] = 0, all[e] = 0;
+  for (int e = tid; e < E; e += kOrderThreads) before[e] = 0, all[e] = 0;
   __syncthreads();
   // two experts to a thread, so that few loads, all under way at once, take a stretch's counts
-  const int words = counts_pitch(E) / 2, wide = (words + 63) / 64 * 64, slices = kThreads / wide, slice = tid / wide, w = tid % wide;
+  const int words = counts_pitch(E) / 2, wide = (words + 63) / 64 * 64, slices = kOrderThreads / wide, slice = tid / wide, w = tid % wide;
   if (slice < slices && w < words) {
     int x[2] = {0, 0}, y[2] = {0, 0};
     constexpr int AHEAD = 32;
@@ -505,19 +535,25 @@ __global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passe
       }
   }
   __syncthreads();
-  const int mine = tid < E ? all[tid] : 0;
-  const int start = block_before(mine, total);
-  if (tid < E) {
-    before[tid] += start;
-    if (b == 0) {
-      a.offsets[tid] = start;
-      if (tid == E - 1) a.offsets[E] = start + mine;
+  constexpr int PER = WQ_MAX_EXPERTS / kOrderThreads;  // experts of a thread
+  int each[PER], sum = 0;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) sum += each[u] = tid * PER + u < E ? all[tid * PER + u] : 0;
+  int start = block_before(sum, total);
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int e = tid * PER + u;
+    if (e < E) {
+      before[e] += start;
+      if (b == 0) a.offsets[e] = start;
+      start += each[u];
+      if (b == 0 && e == E - 1) a.offsets[E] = start;
     }
   }
   __syncthreads();
   for (int i = tid; i < choices;) {
     const int c = next, at = i;
-    i += kThreads;
+    i += kOrderThreads;
     next = i < choices ? places[i] : -1;
     if (c == -1) continue;
     const int p = before[(uint32_t)c >> kRankBits] + (c & ((1 << kRankBits) - 1));
@@ -526,11 +562,16 @@ __global__ __launch_bounds__(kThreads) void k_route_order(RouteArgs a, int passe
   }
 }
 
-template <int L, int R, bool LOOSE = false>
+template <int L, int R, class K, int THREADS, bool LOOSE>
+hipError_t launch_one(const RouteArgs& a, const Layout& at, const Stretches& st, hipStream_t s) {
+  const size_t smem = LOOSE ? (size_t)(THREADS / L) * a.groups * sizeof(typename K::T) : 0;
+  return launch(k_route<L, R, K, LOOSE, THREADS>, dim3((unsigned)st.count), THREADS, smem, s, a, at, st.span, st.passes);
+}
+template <int L, int R, int THREADS, bool LOOSE = false>
 hipError_t route_launch(const RouteArgs& a, const Layout& at, const Stretches& st, bool wide, hipStream_t s) {
-  const size_t smem = LOOSE ? (size_t)(kThreads / L) * a.groups * (wide ? 8 : 4) : 0;
-  return launch(wide ? k_route<L, R, Wide, LOOSE> : k_route<L, R, Narrow, LOOSE>, dim3((unsigned)st.count), kThreads, smem, s, a, at,
-                st.passes);
+  // (16 fp64 keys a lane do not fit the registers that 16 waves on a CU leave: 16384 of 256 experts 31.1 us, 28.9 with 8)
+  constexpr int WIDE_THREADS = R == 16 && L == 16 ? THREADS / 2 : THREADS;
+  return wide ? launch_one<L, R, Wide, WIDE_THREADS, LOOSE>(a, at, st, s) : launch_one<L, R, Narrow, THREADS, LOOSE>(a, at, st, s);
 }
 
 __global__ void k_no_tokens(int32_t* offsets, int n) {
@@ -542,8 +583,10 @@ __global__ void k_no_tokens(int32_t* offsets, int n) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   if (a.M == 0) return launch(k_no_tokens, dim3(1), 256, 0, s, a.offsets, a.E + 1);
   const bool wide = a.bias || a.pairs;
-  const Stretches st = stretches(a.M);
-  // the fewest lanes that hold a token's experts, in the fewest registers
+  Stretches st = stretches(a.M);
+  // one launch of one workgroup where that takes no longer than two: 64 tokens of 128 experts 8.4 us; by biased scores, 64
+  // of 256 in groups, it took 20
+  if (a.M > kFewSpan && a.M <= kSpan && !wide) st = {kSpan, 1, 1};
   const bool on_lanes = (a.groups & (a.groups - 1)) == 0;
   auto fits = [&](int lanes, int regs, Layout& at) {
     if (a.top > lanes || (on_lanes && a.groups > lanes)) return false;
@@ -556,22 +599,34 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   };
   Layout at;
   hipError_t e = hipErrorInvalidValue;
-  const bool few = a.M <= kThreads / 64;
-  if (!on_lanes) e = fits(64, 4, at) ? route_launch<64, 4, true>(a, at, st, wide, s) : fits(64, 16, at) ? route_launch<64, 16, true>(a, at, st, wide, s) : e;
-  else if (few && fits(64, 1, at)) e = route_launch<64, 1>(a, at, st, wide, s);
-  else if (few && fits(64, 2, at)) e = route_launch<64, 2>(a, at, st, wide, s);
-  else if (few && fits(64, 4, at)) e = route_launch<64, 4>(a, at, st, wide, s);
-  else if (fits(16, 1, at)) e = route_launch<16, 1>(a, at, st, wide, s);
-  else if (fits(16, 2, at)) e = route_launch<16, 2>(a, at, st, wide, s);
-  else if (fits(16, 4, at)) e = route_launch<16, 4>(a, at, st, wide, s);
-  else if (fits(16, 8, at)) e = route_launch<16, 8>(a, at, st, wide, s);
-  else if (fits(16, 16, at)) e = route_launch<16, 16>(a, at, st, wide, s);
-  else if (fits(32, 4, at)) e = route_launch<32, 4>(a, at, st, wide, s);
-  else if (fits(32, 16, at)) e = route_launch<32, 16>(a, at, st, wide, s);
-  else if (fits(64, 4, at)) e = route_launch<64, 4>(a, at, st, wide, s);
-  else if (fits(64, 16, at)) e = route_launch<64, 16>(a, at, st, wide, s);
+#define WQ_ROUTE(L, R, T) \
+  if (fits(L, R, at)) e = route_launch<L, R, T>(a, at, st, wide, s)
+  if (!on_lanes) {
+    if (fits(64, 4, at)) e = route_launch<64, 4, 1024, true>(a, at, st, wide, s);
+    else if (fits(64, 16, at)) e = route_launch<64, 16, 1024, true>(a, at, st, wide, s);
+  } else if (a.M <= 4) {
+    // a token to a wave, in a workgroup of no more waves than that takes: 1 token of 128 experts 5.1 us, 6.2 with 16 waves
+    WQ_ROUTE(64, 2, 256);
+    else WQ_ROUTE(64, 4, 256);
+    else WQ_ROUTE(64, 16, 256);
+  } else if (st.span == kFewSpan) {
+    WQ_ROUTE(64, 1, 1024);
+    else WQ_ROUTE(64, 2, 1024);
+    else WQ_ROUTE(64, 4, 1024);
+    else WQ_ROUTE(64, 16, 1024);
+  } else {
+    // the fewest lanes that hold a token's experts, in the fewest registers
+    WQ_ROUTE(16, 1, 1024);
+    else WQ_ROUTE(16, 2, 1024);
+    else WQ_ROUTE(16, 4, 1024);
+    else WQ_ROUTE(16, 8, 1024);
+    else WQ_ROUTE(16, 16, 1024);
+    else WQ_ROUTE(32, 16, 1024);
+    else WQ_ROUTE(64, 16, 1024);
+  }
+#undef WQ_ROUTE
   if (e != hipSuccess || (st.count == 1 && st.passes == 1)) return e;
-  return launch(k_route_order, dim3((unsigned)st.count), kThreads, 0, s, a, st.passes);
+  return launch(k_route_order, dim3((unsigned)st.count), kOrderThreads, 0, s, a, st.span * st.passes);
 }
 
 }  // namespace wq
