@@ -1,14 +1,15 @@
-"""A mixture-of-experts feed-forward layer on the block-scaled FP8 operators.
+"""A mixture-of-experts feed-forward layer on the block-scaled FP8 or the 8-bit integer operators.
 
-    python examples/moe_layer.py [--tokens 64] [--hidden 2048] [--inner 1024] [--experts 32] [--top 4] [--steps 20]
+    python examples/moe_layer.py [--tokens 64] [--hidden 2048] [--inner 1024] [--experts 32] [--top 4] [--steps 20] [--format fp8]
 
 One decoder layer's second half, as a serving loop runs it: the residual
 addition and the RMS norm leave the normalized rows as FP8 codes (and in bf16
-for the router), the router sorts the tokens' choices by expert, each expert's
-gate and up projections are one grouped product over its rows, the gated
-activation leaves codes again, a second grouped product brings them back, and
-the choices are summed with the router's weights.  Weights are random; nothing
-is read back to the host between the steps.
+for the router, and for rows in 8-bit integers), the router picks each token's
+experts and sorts the choices by expert, each expert's gate and up projections
+are one grouped product over its rows, the gated activation leaves codes again,
+a second grouped product brings them back, and the choices are summed with the
+router's weights.  Weights are random; nothing is read back to the host between
+the steps.
 """
 
 import argparse
@@ -19,40 +20,34 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from weight_only_bit_dequant_amd import block  # noqa: E402
+from weight_only_bit_dequant_amd import block, experts, int8  # noqa: E402
 
 
 class MoELayer:
-    """Experts' weights in codes; ``gate_up`` [E, 2 inner, hidden], ``down`` [E, hidden, inner], both bf16."""
+    """Experts' weights in codes; ``gate_up`` [E, 2 inner, hidden], ``down`` [E, hidden, inner], both bf16; ``ops``: block or int8."""
 
-    def __init__(self, gain, router, gate_up, down, top, eps=1e-5):
-        self.gain, self.router, self.top, self.eps = gain, router, top, eps
+    def __init__(self, gain, router, gate_up, down, top, eps=1e-5, ops=block):
+        self.gain, self.router, self.top, self.eps, self.ops = gain, router, top, eps, ops
         self.experts = router.shape[0]
-        self.gate_up, self.down = block.quantize_weight(gate_up), block.quantize_weight(down)
+        self.gate_up, self.down = ops.quantize_weight(gate_up), ops.quantize_weight(down)
 
     def route(self, y):
-        """(weights [M, top], row of each sorted choice, offsets, place of each choice among the sorted)."""
-        prob, pick = (y.float() @ self.router.float().t()).softmax(-1).topk(self.top, dim=-1)
-        order = torch.argsort(pick.reshape(-1), stable=True)
-        offsets = torch.zeros(self.experts + 1, dtype=torch.int32, device=y.device)
-        offsets[1:] = (pick.reshape(-1, 1) == torch.arange(self.experts, device=y.device)).sum(0).cumsum(0)
-        place = torch.empty_like(order)
-        place[order] = torch.arange(order.numel(), device=y.device)
-        return prob / prob.sum(-1, keepdim=True), (order // self.top).to(torch.int32), offsets, place
+        """Each token's experts and weights, and the order that sorts the choices by expert."""
+        return experts.route(y.float() @ self.router.float().t(), self.top)
 
     def __call__(self, x, residual):
         """bf16 x, residual [M, hidden] -> (layer output, new residual)."""
         y = torch.empty_like(x)
         xq, xs, residual, _ = block.add_rmsnorm_quantize(x, self.gain, self.eps, residual=residual, y_out=y)
-        prob, rows, offsets, place = self.route(y)
-        gu = block.grouped_linear(xq, xs, self.gate_up, offsets, rows=rows)
-        hq, hs = block.silu_mul_quantize(gu)
-        z = block.grouped_linear(hq, hs, self.down, offsets)
-        z = z[place].view(x.shape[0], self.top, -1).float()
-        return (z * prob[..., None]).sum(1).to(torch.bfloat16), residual
+        if self.ops is int8:
+            xq, xs = int8.quantize_act(y)
+        r = self.route(y)
+        gu = self.ops.grouped_linear(xq, xs, self.gate_up, r.offsets, rows=r.rows)
+        z = self.ops.grouped_linear(*self.ops.silu_mul_quantize(gu), self.down, r.offsets)
+        return experts.combine(z, r.places, r.weights), residual
 
 
-def random_layer(hidden, inner, experts, top, seed=0, device="cuda"):
+def random_layer(hidden, inner, experts, top, seed=0, device="cuda", ops=block):
     g = torch.Generator(device=device).manual_seed(seed)
 
     def draw(*shape, scale=1.0):
@@ -61,7 +56,7 @@ def random_layer(hidden, inner, experts, top, seed=0, device="cuda"):
     gain = (1 + 0.1 * torch.randn(hidden, generator=g, device=device)).to(torch.bfloat16)
     weights = (draw(experts, hidden, scale=hidden**-0.5), draw(experts, 2 * inner, hidden, scale=hidden**-0.5),
                draw(experts, hidden, inner, scale=inner**-0.5))
-    return MoELayer(gain, *weights, top), weights, draw
+    return MoELayer(gain, *weights, top, ops=ops), weights, draw
 
 
 def float_layer(layer, weights, x, residual):
@@ -69,22 +64,23 @@ def float_layer(layer, weights, x, residual):
     router, gate_up, down = (w.float() for w in weights)
     h = x.float() + residual.float()
     y = h * torch.rsqrt((h * h).mean(-1, keepdim=True) + layer.eps) * layer.gain.float()
-    prob, rows, offsets, place = layer.route(y.to(torch.bfloat16))
-    z = torch.empty(rows.numel(), h.shape[1], device=h.device)
-    off = offsets.tolist()
+    r = layer.route(y.to(torch.bfloat16))
+    z = torch.empty(r.rows.numel(), h.shape[1], device=h.device)
+    off = r.offsets.tolist()
     for e in range(layer.experts):
         if off[e] < off[e + 1]:
-            gate, up = (y[rows[off[e]:off[e + 1]].long()] @ gate_up[e].t()).chunk(2, dim=-1)
+            gate, up = (y[r.rows[off[e]:off[e + 1]].long()] @ gate_up[e].t()).chunk(2, dim=-1)
             z[off[e]:off[e + 1]] = (torch.nn.functional.silu(gate) * up) @ down[e].t()
-    return (z[place].view(h.shape[0], layer.top, -1) * prob[..., None]).sum(1), h
+    return (z[r.places.long()] * r.weights[..., None]).sum(1), h
 
 
 def main():
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     for name, value in dict(tokens=64, hidden=2048, inner=1024, experts=32, top=4, steps=20).items():
         p.add_argument("--" + name, type=int, default=value)
+    p.add_argument("--format", choices=("fp8", "int8"), default="fp8")
     a = p.parse_args()
-    layer, weights, draw = random_layer(a.hidden, a.inner, a.experts, a.top)
+    layer, weights, draw = random_layer(a.hidden, a.inner, a.experts, a.top, ops=int8 if a.format == "int8" else block)
     x, residual = draw(a.tokens, a.hidden), draw(a.tokens, a.hidden, scale=4.0)
     out, h = layer(x, residual)
     want, want_h = float_layer(layer, weights, x, residual)

@@ -13,6 +13,8 @@ Each page quantizes a model in place and then calls it:
     ``quantize_static_fp8(model, (example_input,), calibration_steps=10)``
   * block-scaled FP8 (a scale for each 128 codes; no page):
     ``quantize_linear_fp8_block(model)``
+  * 8-bit integers (a scale for each token and each output channel; no page):
+    ``quantize_linear_int8(model)``
 
 Every ``nn.Linear`` in the model is replaced by a module that holds the packed
 weight and runs the library's kernels in ``forward``; the weight is packed once
@@ -21,7 +23,7 @@ and never refit.  Modules run on the GPU only: there is no CPU path.
 
 import torch
 
-from . import block, wq
+from . import block, int8, wq
 
 _CODES = {"int4": "int4", "nvfp4": "nvfp4", "fp8": "fp8", "mxfp4": "mxfp4"}
 
@@ -110,6 +112,23 @@ class BlockFP8Linear(torch.nn.Module):
         return y.reshape(*lead, self.out_features)
 
 
+class Int8Linear(torch.nn.Module):
+    """8-bit integer Linear: activations quantized on every call with a scale for
+    each token, weights with one for each output channel, the product on the int8
+    matrix cores (``wq_int8_quantize_act``, ``wq_int8_linear``)."""
+
+    def __init__(self, linear):
+        super().__init__()
+        self.in_features, self.out_features = linear.in_features, linear.out_features
+        self.q = int8.quantize_weight(linear.weight.detach().to(torch.bfloat16).contiguous())
+        self.bias = _bias(linear)
+
+    def forward(self, x):
+        x2, lead = _as_2d(x)
+        y = int8.linear(*int8.quantize_act(x2), self.q, self.bias)
+        return y.reshape(*lead, self.out_features)
+
+
 def _swap(model, make):
     """Replace every nn.Linear under `model` (in place) by make(linear, name)."""
     if isinstance(model, torch.nn.Linear):
@@ -144,6 +163,10 @@ def quantize_linear_mxfp4(model, dynamic_activation=False):
 
 def quantize_linear_fp8_block(model):
     return _swap(model, lambda lin, _: BlockFP8Linear(lin))
+
+
+def quantize_linear_int8(model):
+    return _swap(model, lambda lin, _: Int8Linear(lin))
 
 
 @torch.no_grad()
