@@ -600,6 +600,7 @@ hipError_t run_form(Int8Form form, const Int8GemmArgs& a, hipStream_t s) {
     case kI8Stream16: return stream_launch<1, 1, 8>(a, s);
     case kI8Stream16Deep: return stream_launch<1, 1, 8, 2>(a, s);
     case kI8Stream32: return stream_launch<2, 1, 4>(a, s);
+    case kI8Stream16x32: return stream_launch<1, 2, 8>(a, s);
     case kI8Tile256: return tile_launch<Tile256, Tile128>(a, s);
     case kI8Tile256x128: return tile_launch<Tile256x128, Tile128>(a, s);
     case kI8Tile128: return tile_launch<Tile128, Tile128>(a, s);

@@ -29,7 +29,7 @@ hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s);
 // Kernel forms of the products: dot products for single rows (by a wave's columns), streams of the weights for few
 // (by columns x rows of a workgroup; deep: two blocks of a wave under way), LDS tiles for more.
 enum Int8Form {
-  kI8Dot2, kI8Dot4, kI8Dot8, kI8Stream16, kI8Stream16Deep, kI8Stream32,
+  kI8Dot2, kI8Dot4, kI8Dot8, kI8Stream16, kI8Stream16Deep, kI8Stream32, kI8Stream16x32,
   kI8Tile256, kI8Tile256x128, kI8Tile128, kI8Tile128x64, kI8Tile64, kI8Tile32x64, kI8Forms
 };
 // The form of T rows of Y over E experts (a plain Linear: grouped false), chosen on the host (wq_int8_plan.cpp).
