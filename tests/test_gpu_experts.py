@@ -304,6 +304,7 @@ def test_refusals():
         lambda: experts.route(l, 2, valid=torch.ones(5, dtype=torch.bool, **f32)),
         lambda: experts.route(l, 2, valid=torch.ones(6, **f32)),
         lambda: experts.route(l, 2, scale="x"),
+        lambda: experts.route(l, 2, renormalize=torch.ones(2)),  # neither true nor false
         lambda: experts.route(l, 2, out=b._replace(ids=b.ids.long())),
         lambda: experts.route(l, 2, out=b._replace(rows=b.rows[:-1])),
         lambda: experts.route(torch.zeros(2, 1025, **f32), 2),

@@ -25,6 +25,15 @@ int64_t whole(PyObject* o, const char* name) {
   return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refused(std::string(name) + " must be true or false");
+  }
+  return v != 0;
+}
+
 // (logits, top, score, bias, groups, keep, pairs, renormalize, scale, valid, ids, weights, offsets, rows, places, workspace)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 16, [&] {
@@ -55,7 +64,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bytes = (size_t)w.numel();
     }
     const int64_t score = whole(a[2], "score"), groups = whole(a[4], "groups"), keep = whole(a[5], "keep_groups");
-    const int pairs = PyObject_IsTrue(a[6]) > 0, renorm = PyObject_IsTrue(a[7]) > 0;
+    const int pairs = truth(a[6], "pairs"), renorm = truth(a[7], "renormalize");
     return on(dev, [&](void* s) {
       return p_route(l.data_ptr(), half ? 16 : 32, ld, M, E, top, (int)score, (const float*)bias, groups, keep, pairs,
                      renorm, (float)scale, valid, (int32_t*)ids, (float*)weights, (int32_t*)offsets, (int32_t*)rows,
