@@ -94,6 +94,20 @@ def test_route_many_tokens(M, E, top):
     check_route(logits_of(M, E, M, True), top, valid=valid)
 
 
+@pytest.mark.parametrize("E,top,G,keep,pairs,bias", [(16, 2, 1, 1, False, True), (30, 6, 1, 1, False, True), (60, 3, 4, 2, True, True), (64, 16, 8, 4, True, False),
+                                                     (100, 4, 1, 1, False, True), (128, 8, 8, 3, True, True), (120, 12, 2, 1, True, True),
+                                                     (160, 6, 8, 3, False, True), (256, 8, 8, 4, True, True), (256, 3, 16, 5, True, False), (252, 16, 4, 3, True, True),
+                                                     (320, 8, 16, 4, True, True), (512, 4, 32, 9, True, True), (510, 20, 2, 1, False, True), (1024, 8, 8, 4, True, True)])
+def test_route_many_tokens_by_biased_scores(E, top, G, keep, pairs, bias):
+    """Every layout of experts over lanes that many tokens take, both scores."""
+    case(f"route many, biased, {E} top {top} {keep} of {G}")
+    b = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)) if bias else None
+    kw = dict(groups=G, keep_groups=keep, group_score="top2" if pairs else "max")
+    for M, score, renormalize, half in ((4097, "sigmoid", True, False), (4200, "softmax", False, True)):
+        valid = torch.rand(M, generator=torch.Generator().manual_seed(M)) < 0.9 if half else None
+        check_route(logits_of(M, E, M + E, half), top, valid=valid, bias=b, score=score, renormalize=renormalize, **kw)
+
+
 def test_route_one_expert_takes_all():
     case("route one expert takes all")
     l = logits_of(300, 32, 5)
@@ -102,8 +116,8 @@ def test_route_one_expert_takes_all():
     assert int(r.offsets[8] - r.offsets[7]) == 300
 
 
-def test_route_ties_masks_and_nan():
-    case("route ties, masks, NaN")
+def odd_logits():
+    """16 tokens of 40 experts: ties, masks, infinities, NaN, scores that underflow."""
     inf, nan = float("inf"), float("nan")
     l = torch.zeros(16, 40)
     l[1] = -inf
@@ -122,6 +136,14 @@ def test_route_ties_masks_and_nan():
     l[13], l[13, 17] = -inf, inf
     l[14] = torch.finfo(torch.float32).max
     l[15] = -200.0
+    return l
+
+
+@pytest.mark.parametrize("repeat", [1, 257])
+def test_route_ties_masks_and_nan(repeat):
+    case(f"route ties, masks, NaN x {repeat}")
+    inf, nan = float("inf"), float("nan")
+    l = odd_logits().repeat(repeat, 1)
     for kw in (dict(), dict(renormalize=False), dict(score="sigmoid"), dict(score="sigmoid", renormalize=False), dict(groups=5, keep_groups=2),
                dict(groups=8, keep_groups=2), dict(groups=8, keep_groups=3, group_score="top2", score="sigmoid"), dict(groups=10, keep_groups=1, group_score="top2")):
         for top in (1, 6):
@@ -132,6 +154,13 @@ def test_route_ties_masks_and_nan():
             check_route(l, top, bias=bias, **kw)
     bias[11] = nan
     check_route(l, 3, bias=bias)
+    bias[20], bias[4] = inf, -inf
+    check_route(l, 6, bias=bias, score="sigmoid")
+    check_route(l, 6, bias=bias, groups=8, keep_groups=3, group_score="top2")
+    # more experts to a lane
+    check_route(torch.cat([l, l.flip(1), l * 0.5], 1), 8, bias=torch.cat([bias, bias.flip(0), torch.zeros(40)]), score="sigmoid", groups=8, keep_groups=2, group_score="top2")
+    check_route(torch.cat([l] * 6, 1), 9, bias=torch.cat([bias] * 6))
+    check_route(torch.cat([l] * 8, 1), 5, bias=torch.zeros(320), groups=4, keep_groups=3)
 
 
 def test_route_strides():
@@ -158,8 +187,9 @@ def test_route_near_choices():
     g = torch.Generator().manual_seed(4)
     l = torch.full((50, E), 0.75)
     bias = (torch.randperm(E, generator=g).float() - 32) * 2.0**-30
-    check_route(l, 8, bias=bias, score="sigmoid")
-    check_route(l, 8, bias=bias)
+    for many in (l, l.repeat(90, 1)):
+        check_route(many, 8, bias=bias, score="sigmoid")
+        check_route(many, 8, bias=bias)
 
 
 # ---------------------------------------------------------------- combine

@@ -281,7 +281,8 @@ __device__ __forceinline__ int better_groups(typename K::T v, int group, int lan
       constexpr int BY = decltype(by)::value;
       if (BY % lanes) return;  // (uniform)
       const typename K::T o = dpp<0x120 + BY>(v);
-      better += o > v || (o == v && dpp<0x120 + BY>(group) < group);
+      const int g = dpp<0x120 + BY>(group);  // (from all lanes, not those with a tie alone)
+      better += o > v || (o == v && g < group);
     });
   } else {
     for (int g = 0; g < groups; ++g) {
