@@ -45,7 +45,8 @@ enum {
  *   any number, and equal to any NaN.  A softmax over a NaN or +infinity is NaN
  *   throughout.
  *   Scores that a bias or pairs compare, and weights' ratios, are held in fp64;
- *   a softmax sum that only weights need in fp32.
+ *   a softmax sum that only weights need in fp32.  Choices of scores may
+ *   count as equal where they differ by less than 2^-43 of their size.
  *
  *   logits   : fp32 (logit_bits 32) or bf16 (16), row m at logits + m * ld elements, E <= ld < 2^22
  *   bias     : fp32 [E] or NULL

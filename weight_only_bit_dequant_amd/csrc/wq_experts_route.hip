@@ -17,10 +17,12 @@
 // the second each workgroup adds up the counts before its own.
 //
 // What bounds it: 16384 tokens of 256 experts (sigmoid, bias, the best 4 of 8 groups)
-// take 24 us in the first launch, instructions: of some 1900 for four tokens half are
-// the eight picks, a quarter the scores in fp64.  The second takes 7 us, a few trips to
-// memory.  By the logits alone the first takes 11 us.  One token takes 4.9 us, 2.5 of
-// them the launch, one trip to memory, and the picks one after the other.
+// take 20 us in the first launch, instructions: of some 1500 for four tokens a third
+// are the scores in fp64, a third the order in each lane and the eight picks (the next
+// tokens' logits fetched ahead, four scores' chains side by side: no change).  The second
+// takes 7 us, a few trips to memory.  By the logits alone the first takes 12 us.  One
+// token takes 4.9 us, 2.5 of them the launch, one trip to memory, and the picks one
+// after the other.
 #include <type_traits>
 #include <utility>
 
@@ -52,11 +54,11 @@ struct Narrow {
   __device__ __forceinline__ static T min(T a, T b) { return a < b ? a : b; }
   __device__ __forceinline__ static T sum(T a, T) { return a; }  // (pairs are never narrow)
 };
-// Choices as fp64 numbers: -infinity is not to be picked, NaN is +infinity and
-// +infinity the largest number (choices of fp32 biases are far below it).
+// Choices as fp64 numbers: what is not to be picked, +infinity and NaN are powers of
+// two (2^1010, negative, 2^1000 and 2^1010; choices of fp32 biases are far below them).
 struct Wide {
   typedef double T;
-  static constexpr T kNot = -__builtin_inf(), kMost = 1.7976931348623157e308;
+  static constexpr T kNaN = 0x1p1010, kNot = -kNaN, kMost = 0x1p1000;
   // (the instructions themselves: the compiler's fmax first makes each operand that might be a signalling NaN a quiet one)
   __device__ __forceinline__ static T max(T a, T b) {
     asm("v_max_f64 %0, %1, %2" : "=v"(a) : "v"(a), "v"(b));
@@ -67,13 +69,65 @@ struct Wide {
     return a;
   }
   __device__ __forceinline__ static T of(double c) {
-    const double m = min(c, kMost);
-    return c != c ? __builtin_inf() : m;
+    const double m = max(min(c, kMost), kNot);
+    return c != c ? kNaN : m;
   }
   __device__ __forceinline__ static T sum(T a, T b) {  // of a group's two largest, a >= b
     return b == kNot ? a : a > kMost ? a : min(a + b, kMost);
   }
 };
+
+// Choices with their expert's number in the low BITS bits (the lowest expert the largest): no two experts' are equal, and
+// the number comes with the choice through maxima and sorting.  That takes 2^-43 or less of a choice: nearer ones are equal.
+template <int BITS>
+struct Numbered {
+  static constexpr uint32_t MASK = (1u << BITS) - 1;
+  // (of negative numbers the smallest number is the largest)
+  __device__ __forceinline__ static uint32_t turned(u32x2 u) { return (uint32_t)((int32_t)u.y >> 31); }
+  __device__ __forceinline__ static double of(double c, int e) {
+    u32x2 u = __builtin_bit_cast(u32x2, c);
+    u.x = (u.x & ~MASK) | (~((uint32_t)e ^ turned(u)) & MASK);
+    return __builtin_bit_cast(double, u);
+  }
+  __device__ __forceinline__ static int expert(double v) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    return (int)(~(u.x ^ turned(u)) & MASK);
+  }
+  __device__ __forceinline__ static double choice(double v) {
+    u32x2 u = __builtin_bit_cast(u32x2, v);
+    u.x &= ~MASK;
+    return __builtin_bit_cast(double, u);
+  }
+};
+
+// The D largest of R numbers, in descending order, in v[0 .. D): blocks of D by Batcher's odd-even merge sort, then
+// each next block's largest: of two ordered blocks the larger of v[i] and w[D - 1 - i], a bitonic sequence, merged.
+template <int R, int D>
+__device__ __forceinline__ void largest(double (&v)[R]) {
+  auto order = [&](int i, int j) {
+    const double a = v[i], b = v[j];
+    v[i] = Wide::max(a, b);
+    v[j] = Wide::min(a, b);
+  };
+#pragma unroll
+  for (int b = 0; b < R; b += D) {
+#pragma unroll
+    for (int p = 1; p < D; p *= 2)
+#pragma unroll
+      for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+        for (int i = 0; i + k < D; ++i)
+          if (i % (2 * k) >= k % p && (i - k % p) % (2 * k) < k && i / (2 * p) == (i + k) / (2 * p)) order(b + i, b + i + k);
+    if (b == 0) continue;
+#pragma unroll
+    for (int i = 0; i < D; ++i) v[i] = Wide::max(v[i], v[b + D - 1 - i]);
+#pragma unroll
+    for (int k = D / 2; k >= 1; k /= 2)
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if (!(i & k)) order(i, i | k);
+  }
+}
 
 // ---------------------------------------------------------------- across lanes
 
@@ -193,25 +247,32 @@ __device__ __forceinline__ double exp64(double x) {
   for (double k : c) p = step(p, k);
   return __builtin_ldexp(p, (int)n);
 }
-// c ? a : b without a branch around what a takes.
+// c ? a : b without a branch around what a takes, or an index of c.
 __device__ __forceinline__ double either(bool c, double a, double b) {
   asm("" : "+v"(a));
   asm("" : "+v"(b));
   return c ? a : b;
 }
-// 1 / (1 + exp(-l)), NaN for NaN, 0 where exp(-l) leaves fp64's range.  The reciprocal is the hardware's with two
-// Newton steps.
-__device__ __forceinline__ double sigmoid64(float l) {
-  constexpr float far = -709.78265f;  // the last fp32 number above -1024 ln 2
-  const double d = 1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l, far, 800.0f));
+// 1 / (1 + exp(-l)) of a number, the same for all below kFar, where exp(-l) leaves fp64's range.  The reciprocal is the
+// hardware's with two Newton steps.
+constexpr float kFar = -709.78265f;  // the last fp32 number above -1024 ln 2
+__device__ __forceinline__ double sigmoid_of_number(float l) {
+  const double d = 1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l, kFar, 800.0f));
   double r = __builtin_amdgcn_rcp(d);
   r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  return either(l != l, __builtin_nan(""), either(l < far, 0.0, r));
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
-// exp(l - peak): 0 for -infinity, NaN where either is NaN or the peak +infinity.
+// The same, NaN for NaN, 0 below kFar.
+__device__ __forceinline__ double sigmoid64(float l) {
+  return either(l != l, __builtin_nan(""), either(l < kFar, 0.0, sigmoid_of_number(l)));
+}
+// exp(l - peak) of a finite peak, 0 for l of -infinity.
+__device__ __forceinline__ double below_finite_peak(float l, float peak) {
+  return exp64(Wide::max((double)l - (double)peak, -800.0));
+}
+// The same, NaN where either is NaN or the peak +infinity.
 __device__ __forceinline__ double below_peak64(float l, float peak) {
-  const double e = exp64(__builtin_fmax((double)l - (double)peak, -800.0));
+  const double e = below_finite_peak(l, peak);
   return either(l == -__builtin_inff(), 0.0, either(l != l, __builtin_nan(""), e + ((double)peak - (double)peak)));
 }
 
@@ -295,7 +356,11 @@ __device__ __forceinline__ int better_groups(typename K::T v, int group, int lan
   return better;
 }
 
-template <int L, int R, class K, bool LOOSE, int THREADS>
+// D = 0: each pick looks through all choices of the lanes.  D > 0, of fp64 choices: each lane orders its D largest (as many
+// as are picked, or all it has) first, and a pick is the largest of the lanes' first ones.  16384 of 256 experts by biased
+// scores: 29.4 -> 25.1 us, in groups 31.7 -> 27.1, of 512 53 -> 40; by logits, whose keys take half the registers, 20.2 -> 19.5
+// for 8 picks and 26.6 -> 31.3 for 16.
+template <int L, int R, int D, class K, bool LOOSE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int span, int passes) {
   typedef typename K::T T;
   constexpr bool WIDE = sizeof(T) == 8;
@@ -315,9 +380,13 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
   const int in_group = l % at.lanes, group = l / at.lanes;
   const int first = group * at.per + in_group * at.q;
   const int mine = max(0, min(at.q, min(at.per - in_group * at.q, E - first)));
-  float bias[WIDE ? R : 1];
-  if constexpr (WIDE)
-    load_run<R>(make_rsrc(a.bias, a.bias ? (uint32_t)E * 4u : 0u), (uint32_t)first * 4u, mine, false, at.whole, -__builtin_inff(), bias);
+  T bias[WIDE ? R : 1];  // kNot past a lane's experts
+  if constexpr (WIDE) {
+    float b[R];
+    load_run<R>(make_rsrc(a.bias, a.bias ? (uint32_t)E * 4u : 0u), (uint32_t)first * 4u, mine, false, at.whole, -__builtin_inff(), b);
+#pragma unroll
+    for (int r = 0; r < R; ++r) bias[r] = K::of((double)b[r]);
+  }
 
   for (int pass = 0; pass < passes; ++pass) {
     const int64_t m0 = ((int64_t)blockIdx.x * passes + pass) * span;
@@ -336,7 +405,7 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
       {
         float logit[R];
         load_run<R>(rows, ((uint32_t)t * (uint32_t)a.ld + (uint32_t)first) * (a.half ? 2u : 4u), live ? mine : 0, a.half, at.whole,
-                    -__builtin_inff(), logit);
+                    WIDE && a.sigmoid && live ? 0.f : -__builtin_inff(), logit);
         if (!a.sigmoid || !WIDE) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -348,24 +417,38 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
         }
         peak = Narrow::logit(biggest);
         if constexpr (WIDE) {
-          double part = 1.0;
+          // choices of numbers; infinities and NaN, if the wave has any, after that (a logit of +infinity has the score 1)
+          constexpr int kNaNs = 0x003, kBelow = 0x004, kAbove = 0x200;
+          bool odd;
           if (a.sigmoid) {
+            odd = false;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              key[r] = sigmoid64(logit[r]);
+              key[r] = sigmoid_of_number(logit[r]) + bias[r];
+              odd |= __builtin_amdgcn_classf(logit[r], kNaNs | kBelow);
               if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (16 at once would not fit the registers)
             }
           } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              sum += key[r] = below_peak64(logit[r], peak);
+              sum += key[r] = below_finite_peak(logit[r], peak);
               if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
             sum = sum_over(sum, L);
-            part = 1.0 / sum;
-          }
+            const double part = 1.0 / sum;
+            odd = __builtin_amdgcn_classf(peak, kNaNs | kBelow | kAbove);
 #pragma unroll
-          for (int r = 0; r < R; ++r) key[r] = either(logit[r] == -__builtin_inff(), K::kNot, K::of(key[r] * part + (double)bias[r]));
+            for (int r = 0; r < R; ++r) {
+              key[r] = __builtin_fma(key[r], part, bias[r]);
+              odd |= __builtin_amdgcn_classf(logit[r], kBelow);
+            }
+          }
+          if (__any(odd)) {
+            const bool all = !a.sigmoid && __builtin_amdgcn_classf(peak, kNaNs | kAbove);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              key[r] = either(logit[r] == -__builtin_inff(), K::kNot, either(all || logit[r] != logit[r], K::kNaN, key[r]));
+          }
         } else if (!a.sigmoid && !a.renormalize) {
           float each = 0.f;
 #pragma unroll
@@ -374,62 +457,85 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
         }
       }
 
-      if (a.groups > 1) {
-        if constexpr (!LOOSE) {
-          Two<K> two{K::kNot, K::kNot};
-#pragma unroll
-          for (int r = 0; r < R; ++r) two.add(key[r]);
-          const T v = group_value<K>(two, at.lanes, a.pairs);
-          if (better_groups<L, K>(v, group, at.lanes, a.groups, tid & 63) >= a.keep) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) key[r] = K::kNot;
-          }
-        } else {
-          T* value = reinterpret_cast<T*>(loose) + slot * a.groups;
-          const int size = E / a.groups;
-          for (int g = 0; g < a.groups; ++g) {
-            Two<K> t2{K::kNot, K::kNot};
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-              if ((first + r) / size == g) t2.add(key[r]);
-            const T v = group_value<K>(t2, L, a.pairs);
-            if (l == 0) value[g] = v;
-          }
-          __syncthreads();
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= mine) continue;
-            const int own = (first + r) / size;
-            const T v = value[own];
-            int better = 0;
-            for (int g = 0; g < a.groups; ++g) better += value[g] > v || (value[g] == v && g < own);
-            if (better >= a.keep) key[r] = K::kNot;
-          }
-          __syncthreads();
-        }
-      }
-
       int pick = -1;  // of lane j: the j-th largest choice
       float x = 0.f;  // its logit
-      for (int j = 0; j < top; ++j) {
-        T best = key[0];
+      if constexpr (D > 0) {
+        typedef Numbered<__builtin_ctz(L * R)> N;
 #pragma unroll
-        for (int r = 1; r < R; ++r) best = K::max(best, key[r]);
-        best = max_over<K>(best, L);
-        uint32_t e = ~0u;  // the lowest expert of that key
+        for (int r = 0; r < R; ++r) key[r] = N::of(key[r], first + r);
+        largest<R, D>(key);
+        if (a.groups > 1) {
+          const double of_group = group_value<K>(Two<K>{N::choice(key[0]), N::choice(key[1])}, at.lanes, a.pairs);
+          if (better_groups<L, K>(of_group, group, at.lanes, a.groups, tid & 63) >= a.keep) {
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(first + r) : e;
-        if constexpr (L == 64) {
-          e = __builtin_amdgcn_readlane(e, __builtin_ctzll(__ballot(e != ~0u)));
-        } else {
-          e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+            for (int r = 0; r < D; ++r) key[r] = K::kNot;
+          }
         }
-        if (l == j && best != K::kNot) {
-          pick = (int)e;
-          if constexpr (!WIDE) x = Narrow::logit(best);
-        }
+        double own = K::kNot;
+        for (int j = 0; j < top; ++j) {
+          const double best = max_over<K>(key[0], L);
+          const bool taken = key[0] == best;
 #pragma unroll
-        for (int r = 0; r < R; ++r) key[r] = (uint32_t)(first + r) == e ? K::kNot : key[r];
+          for (int r = 0; r < D; ++r) key[r] = either(taken, r + 1 < D ? key[r + 1] : K::kNot, key[r]);
+          own = l == j ? best : own;
+        }
+        if (N::choice(own) != K::kNot) pick = N::expert(own);
+      } else {
+        if (a.groups > 1) {
+          if constexpr (!LOOSE) {
+            Two<K> two{K::kNot, K::kNot};
+#pragma unroll
+            for (int r = 0; r < R; ++r) two.add(key[r]);
+            const T v = group_value<K>(two, at.lanes, a.pairs);
+            if (better_groups<L, K>(v, group, at.lanes, a.groups, tid & 63) >= a.keep) {
+#pragma unroll
+              for (int r = 0; r < R; ++r) key[r] = K::kNot;
+            }
+          } else {
+            T* value = reinterpret_cast<T*>(loose) + slot * a.groups;
+            const int size = E / a.groups;
+            for (int g = 0; g < a.groups; ++g) {
+              Two<K> t2{K::kNot, K::kNot};
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+                if ((first + r) / size == g) t2.add(key[r]);
+              const T v = group_value<K>(t2, L, a.pairs);
+              if (l == 0) value[g] = v;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (r >= mine) continue;
+              const int own = (first + r) / size;
+              const T v = value[own];
+              int better = 0;
+              for (int g = 0; g < a.groups; ++g) better += value[g] > v || (value[g] == v && g < own);
+              if (better >= a.keep) key[r] = K::kNot;
+            }
+            __syncthreads();
+          }
+        }
+
+        for (int j = 0; j < top; ++j) {
+          T best = key[0];
+#pragma unroll
+          for (int r = 1; r < R; ++r) best = K::max(best, key[r]);
+          best = max_over<K>(best, L);
+          uint32_t e = ~0u;  // the lowest expert of that key
+#pragma unroll
+          for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(first + r) : e;
+          if constexpr (L == 64) {
+            e = __builtin_amdgcn_readlane(e, __builtin_ctzll(__ballot(e != ~0u)));
+          } else {
+            e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+          }
+          if (l == j && best != K::kNot) {
+            pick = (int)e;
+            if constexpr (!WIDE) x = Narrow::logit(best);
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) key[r] = (uint32_t)(first + r) == e ? K::kNot : key[r];
+        }
       }
       if (WIDE && pick >= 0) x = logit_at(a, m, pick);
 
@@ -563,16 +669,21 @@ __global__ __launch_bounds__(kOrderThreads) void k_route_order(RouteArgs a, int 
   }
 }
 
-template <int L, int R, class K, int THREADS, bool LOOSE>
+template <int L, int R, int D, class K, int THREADS, bool LOOSE>
 hipError_t launch_one(const RouteArgs& a, const Layout& at, const Stretches& st, hipStream_t s) {
   const size_t smem = LOOSE ? (size_t)(THREADS / L) * a.groups * sizeof(typename K::T) : 0;
-  return launch(k_route<L, R, K, LOOSE, THREADS>, dim3((unsigned)st.count), THREADS, smem, s, a, at, st.span, st.passes);
+  return launch(k_route<L, R, D, K, LOOSE, THREADS>, dim3((unsigned)st.count), THREADS, smem, s, a, at, st.span, st.passes);
 }
 template <int L, int R, int THREADS, bool LOOSE = false>
 hipError_t route_launch(const RouteArgs& a, const Layout& at, const Stretches& st, bool wide, hipStream_t s) {
   // (16 fp64 keys a lane do not fit the registers that 16 waves on a CU leave: 16384 of 256 experts 31.1 us, 28.9 with 8)
   constexpr int WIDE_THREADS = R == 16 && L == 16 ? THREADS / 2 : THREADS;
-  return wide ? launch_one<L, R, Wide, WIDE_THREADS, LOOSE>(a, at, st, s) : launch_one<L, R, Narrow, THREADS, LOOSE>(a, at, st, s);
+  if (!wide) return launch_one<L, R, 0, Narrow, THREADS, LOOSE>(a, at, st, s);
+  if constexpr (L < 64 && R >= 8) {
+    if (a.top <= 4) return launch_one<L, R, 4, Wide, WIDE_THREADS, LOOSE>(a, at, st, s);
+    if (a.top <= 8) return launch_one<L, R, 8, Wide, WIDE_THREADS, LOOSE>(a, at, st, s);
+  }
+  return launch_one<L, R, L < 64 && R >= 4 ? R : 0, Wide, WIDE_THREADS, LOOSE>(a, at, st, s);
 }
 
 __global__ void k_no_tokens(int32_t* offsets, int n) {
