@@ -108,6 +108,14 @@ def test_route_many_tokens_by_biased_scores(E, top, G, keep, pairs, bias):
         check_route(logits_of(M, E, M + E, half), top, valid=valid, bias=b, score=score, renormalize=renormalize, **kw)
 
 
+@pytest.mark.parametrize("M,E,top,G", [(17000, 36, 6, 6), (16500, 64, 6, 8), (33000, 24, 2, 1), (17000, 250, 3, 5)])
+def test_route_many_stretches_by_biased_scores(M, E, top, G):
+    """Stretches of several passes; groups that lie over the lanes and groups that do not."""
+    case(f"route stretches, biased, {M} of {E} top {top} of {G}")
+    b = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+    check_route(logits_of(M, E, M), top, bias=b, score="sigmoid", groups=G, keep_groups=(G + 1) // 2, group_score="top2")
+
+
 def test_route_one_expert_takes_all():
     case("route one expert takes all")
     l = logits_of(300, 32, 5)
