@@ -5,6 +5,16 @@
 // forms that split K give the same bits as those that do not.  The weights are
 // operand A, so that a lane holds neighbouring columns n of one row m: one
 // activation scale, four weight scales, 8 bytes of bf16 output at a time.
+//
+// What bounds them, in us of graphs of calls whose weights come from memory:
+//   1 x 4096 x 4096, 16.8 MB                5.5 by dot products: the launch and one trip to memory
+//   48 rows of 64 experts, 1408 x 2048      13: the weights' stream, 98 MB
+//   2800 rows of 64 experts, 1536 x 2048    43: the weights' stream, 4.9 TB/s
+//   333 x 5003 x 2064                       12: 17 steps of 0.4, loads beyond L2 with 96 KB under way; 4 of launch, first loads
+//                                           and stores; rows across two cache lines (K % 128 != 0) are 1.6 of them
+//   4096 x 2048 x 5632                      42 alone, 47 in a row: the matrix cores, busy 70 %, and the power limit
+//   8192 x 8192 x 8192                      424, 2.6 POP/s: the power limit (1.82 GHz, the matrix cores busy 80 % at that
+//                                           clock); their MFMAs on registers alone reach 3.5 POP/s with random codes
 #include "wq_int8_internal.hpp"
 #include "wq_row_tiles.hpp"
 
@@ -105,7 +115,8 @@ __global__ __launch_bounds__(256) void k_int8_dot(Int8GemmArgs a, int gx, int gy
 // its own in LDS (buffer_load ... lds, 8 whole 128-byte rows per instruction) and
 // reads them back as operands; SL slots are blocks under way.  Waves meet once,
 // to add up their sums.  Bound by the weights' stream and, below some 10 MB, by
-// the trips to memory.
+// the trips to memory.  16 columns where the weights are few, so that more
+// workgroups read them; 32 rows at once rather than the weights twice.
 template <int NT, int MT, int W, int SL>
 struct StreamT {
   static constexpr int SLOT = (NT + MT) * 2048, L = 2 * (NT + MT);  // bytes and loads per block
@@ -241,17 +252,26 @@ __global__ __launch_bounds__(W * 64) void k_int8_stream(Int8GemmArgs a, int gx, 
 // A workgroup of WN x WM waves owns BN columns x BM rows of Y; K advances 128 per
 // step, four MFMAs deep.  Operand rows go from memory straight into LDS
 // (buffer_load ... lds: lane i's 16 bytes land at the wave's base + 16 i), 8
-// whole rows of 128 bytes per instruction, NS stages deep; the 16-byte chunks of
-// row r are XOR-swizzled by r / 2 % 8, by the choice of the chunk that each lane
-// loads, so that 32 rows' reads of one chunk fall on distinct banks.
+// whole rows of 128 bytes per instruction; the 16-byte chunks of row r are
+// XOR-swizzled by r / 2 % 8, by the choice of the chunk that each lane loads, so
+// that 32 rows' reads of one chunk fall on distinct banks (conflicts: 3 % of the
+// cycles).  Steps of 64 load half cache lines: 128 x 128 tiles 534 -> 681 us at 8192^3.
+//
+// LDS is a ring of UNITS units, a step's weights or its activations in turn, so
+// that 160 KB hold two and a half steps of a 256 x 256 tile: the loads of two are
+// always under way or landed while one is multiplied.  Smaller tiles have five
+// steps, as their loads' way is long against a step (deeper rings: no change).
 //
 // A wave owns 32 TN x 32 TM of the tile.  Its fragments of a quarter step (K = 32)
 // are read while the quarter before is multiplied, in two sets of registers.  When
 // the last quarter's have been read the waves meet, at the step's one barrier:
-// the stage is free, the next one has landed.  The last quarter's MFMAs cover its
-// first reads of the next stage; its refill is spread over the step that follows.
+// its units are free, the next step's have landed.  The last quarter's MFMAs cover
+// its first reads of the next step; the refill is spread over SPAN quarters (all in
+// one: 465 us, 441 spread, at 8192^3).  Eight waves, two to a SIMD: four take as long
+// on whole tiles (4096 x 2048 x 5632 in 256 x 128: 47 us both) and longer where some
+// of them have no rows (333 x 5000 x 2048: 14.5 and 16.8).
 //
-// With KS > 1, KS such groups of waves split K, each with its own stages, and add
+// With KS > 1, KS such groups of waves split K, each with its own ring, and add
 // up their sums in LDS at the end: tiles too few to fill the chip finish sooner.
 template <int BN_, int BM_, int WN_, int WM_, int KS_, int UNITS_, int SPAN_ = 4>
 struct Tile {
@@ -450,7 +470,7 @@ __device__ __forceinline__ void tile(const Int8GemmArgs& a, const RowTile t, con
     if (vec) {
       if (n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
     } else if (n + 8 <= N) {
-      *reinterpret_cast<u32x4_any*>(y) = v;  // (rows of an odd width start anywhere)
+      *reinterpret_cast<u32x4_any*>(y) = v;  // (rows of an odd width start anywhere; element by element 333 x 5003 x 2064 takes 4 us more)
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
