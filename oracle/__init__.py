@@ -21,6 +21,8 @@ What it implements, and from which passage (the pages are the Torch-TensorRT
   static-FP8 Linear / two-layer model.
 * ``mx_dynamic`` -- dynamic MX quantization of activations and the MXFP4 x
   MXFP4 Linear of the MXFP4 page's "Dynamic Activation + MX Weight" config.
+* ``block``, ``int8``, ``experts`` -- the block-scaled FP8 and the 8-bit integer
+  operators, and the experts' routing (from their formulas; no page has them).
 
 Arithmetic rules used throughout: bf16 inputs widen exactly to fp32; every
 quantizer step is an IEEE fp32 operation (numpy float32, correctly rounded);
