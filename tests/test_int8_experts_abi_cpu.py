@@ -152,7 +152,7 @@ def test_route():
     assert route(M=1 << 29) == wq.EUNSUPPORTED
     assert route(M=1 << 62) == wq.EUNSUPPORTED
     need = experts._lib().wq_experts_route_workspace(65, 12)
-    assert need == 5 * 12 * 2
+    assert need == 17 * 12 * 2  # stretches of four tokens
     assert route(M=65) == wq.EWORKSPACE
     assert route(M=65, WS=4, ws=need - 1) == wq.EWORKSPACE
     assert route(M=65, WS=2, ws=need) == wq.EALIGN

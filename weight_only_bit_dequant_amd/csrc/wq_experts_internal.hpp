@@ -28,12 +28,15 @@ struct RouteArgs {
 
 // Tokens in stretches, one to a workgroup: `passes` times `span` tokens each, at
 // most 2^16 - 64 in all (a stretch's counts have 16 bits).  Few tokens are spread
-// over the chip, a wave to each; many share a wave.
-constexpr int kFewSpan = 16, kSpan = 64, kMaxStretches = 256, kMaxPasses = 1023;
+// over the chip, a wave to each; many share a wave.  Four waves to a workgroup, one
+// to a SIMD, as long as the second launch has no more stretches to add up for it:
+// 256 of 256 experts in groups 14.9 -> 11.5 us, 1000 15.2 -> 14.3, 900 of 60 10.2 -> 9.4.
+constexpr int kWaves = 4, kFewSpan = 16, kSpan = 64, kMaxStretches = 256, kMaxPasses = 1023;
 struct Stretches {
   int span, passes, count;
 };
 inline Stretches stretches(int64_t M) {
+  if (M > kFewSpan && M <= kWaves * kMaxStretches) return {kWaves, 1, (int)((M + kWaves - 1) / kWaves)};
   if (M <= kFewSpan * kMaxStretches) return {kFewSpan, 1, M ? (int)((M + kFewSpan - 1) / kFewSpan) : 1};
   const int64_t all = (M + kSpan - 1) / kSpan, even = (all + kMaxStretches - 1) / kMaxStretches;
   const int64_t passes = even < kMaxPasses ? even : kMaxPasses;

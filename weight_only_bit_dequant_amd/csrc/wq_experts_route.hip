@@ -397,7 +397,7 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
     for (int sub = 0; sub < tokens; sub += AT_ONCE) {
       const int t = sub + slot;
       const int64_t m = m0 + t;
-      const bool live = m < a.M && (!a.valid || a.valid[m]);
+      const bool live = t < tokens && (!a.valid || a.valid[m]);
       T key[R];
       uint32_t biggest = 0;  // key of the row's largest logit
       double sum = 0.0;
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
         s /= sum;
       }
       if (l < top) {
-        if (m < a.M) {
+        if (t < tokens) {
           a.ids[m * top + l] = pick;
           a.weights[m * top + l] = pick >= 0 ? (float)((double)a.scale * s) : 0.f;
         }
@@ -714,11 +714,13 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
 #define WQ_ROUTE(L, R, T) \
   if (fits(L, R, at)) e = route_launch<L, R, T>(a, at, st, wide, s)
   if (!on_lanes) {
-    if (fits(64, 4, at)) e = route_launch<64, 4, 1024, true>(a, at, st, wide, s);
-    else if (fits(64, 16, at)) e = route_launch<64, 16, 1024, true>(a, at, st, wide, s);
-  } else if (a.M <= 4) {
+    const bool waves = st.span == kWaves;
+    if (fits(64, 4, at)) e = waves ? route_launch<64, 4, 256, true>(a, at, st, wide, s) : route_launch<64, 4, 1024, true>(a, at, st, wide, s);
+    else if (fits(64, 16, at)) e = waves ? route_launch<64, 16, 256, true>(a, at, st, wide, s) : route_launch<64, 16, 1024, true>(a, at, st, wide, s);
+  } else if (a.M <= 4 || st.span == kWaves) {
     // a token to a wave, in a workgroup of no more waves than that takes: 1 token of 128 experts 5.1 us, 6.2 with 16 waves
-    WQ_ROUTE(64, 2, 256);
+    WQ_ROUTE(64, 1, 256);
+    else WQ_ROUTE(64, 2, 256);
     else WQ_ROUTE(64, 4, 256);
     else WQ_ROUTE(64, 16, 256);
   } else if (st.span == kFewSpan) {
