@@ -8,7 +8,7 @@
 //
 // What bounds them, in us of graphs of calls whose weights come from memory:
 //   1 x 4096 x 4096, 16.8 MB                5.5 by dot products: the launch and one trip to memory
-//   48 rows of 64 experts, 1408 x 2048      13: the weights' stream, 98 MB
+//   48 rows of 64 experts, 1408 x 2048      11: the weights' stream, 98 MB, some of them from the Infinity Cache
 //   2800 rows of 64 experts, 1536 x 2048    43: the weights' stream, 4.9 TB/s
 //   333 x 5003 x 2064                       12: 17 steps of 0.4, loads beyond L2 with 96 KB under way; 4 of launch, first loads
 //                                           and stores; rows across two cache lines (K % 128 != 0) are 1.6 of them

@@ -3,12 +3,13 @@
 // run another one than they mean when the rule changes.
 //
 // Each form's time is a formula in its tiles and in the blocks of 128 K; the form
-// with the least time is run.  The constants are fitted to the times of all
-// forms over 200 random shapes and 120 grouped ones (1 to 8192 rows, 256 to 8192
-// columns and K, weights from memory, graphs of back-to-back launches); over the
-// same shapes the chosen form took 3 % more than the best one on average, a third
-// at worst.  What the formulas do not see is how uneven the experts are, and that T
-// may be more than there are rows.
+// with the least time is run.  The constants are fitted to the choices over 611 plain
+// shapes and 290 grouped ones, random and powers of two (1 to 8192 rows, 256 to 8192
+// columns and K, weights from memory, graphs of back-to-back launches): over the
+// same shapes the chosen form takes 1.1 % more than the best one on average, 22 % at
+// worst; over a quarter of them that a fit to the others left out, 1.4 and 2.0 %.  What
+// the formulas do not see is how uneven the experts are, and that T may be more than
+// there are rows.
 #include <cmath>
 
 #include "wq_int8_internal.hpp"
@@ -19,21 +20,23 @@ namespace {
 
 // LDS tiles, bn x bm, `at_once` of them on the chip.  Time of a launch in us:
 //   2 + rounds (start + look + blocks per_block) + end
-// with per_block falling to `few` of itself, and the end to nothing, as a round
-// empties; no less than the weights of all experts that have rows from memory.
+// with per_block falling over `half` of itself to `few`, and the end to nothing, as a
+// round is half full and then empties (where two tiles share a CU, a half is one to
+// each: 1024 x 4096 x 4096 in 256 tiles takes 24 us, in 128 of twice the size 31); no
+// less than the weights of all experts that have rows from memory.
 // `look`: for the tile of an expert.  `split`: what K % 128 != 0 adds to a block, whose
 // rows then lie across two cache lines.
 struct TileCost {
   Int8Form form;
   int bn, bm, at_once;
-  float start, per_block, few, memory, look, end, split;  // memory in TB/s
+  float start, per_block, few, half, memory, look, end, split;  // memory in TB/s
 };
-const TileCost kTiles[] = {{kI8Tile256, 256, 256, 256, 6.34f, 1.70f, 0.39f, 6.3f, 0.f, 0.f, 0.02f},
-                           {kI8Tile256x128, 256, 128, 256, 3.51f, 0.975f, 0.34f, 4.8f, 1.30f, 0.86f, 0.20f},
-                           {kI8Tile128, 128, 128, 512, 2.60f, 1.20f, 0.166f, 5.1f, 0.17f, 2.45f, 0.20f},
-                           {kI8Tile128x64, 128, 64, 256, 2.18f, 0.400f, 0.62f, 4.4f, 0.69f, 0.03f, 0.23f},
-                           {kI8Tile64, 64, 64, 512, 1.64f, 0.460f, 0.286f, 4.6f, 0.48f, 0.81f, 0.31f},
-                           {kI8Tile32x64, 32, 64, 256, 1.56f, 0.174f, 0.61f, 3.6f, 0.25f, 0.24f, 0.30f}};
+const TileCost kTiles[] = {{kI8Tile256, 256, 256, 256, 7.76f, 1.58f, 0.121f, 0.83f, 3.87f, 0.367f, 0.026f, 0.0115f},
+                           {kI8Tile256x128, 256, 128, 256, 3.47f, 0.903f, 0.598f, 0.669f, 5.44f, 0.177f, 1.2f, 0.246f},
+                           {kI8Tile128, 128, 128, 512, 1.49f, 1.14f, 0.399f, 0.513f, 7.46f, 0.411f, 3.96f, 0.272f},
+                           {kI8Tile128x64, 128, 64, 256, 1.87f, 0.382f, 0.661f, 0.831f, 4.68f, 0.777f, 0.354f, 0.147f},
+                           {kI8Tile64, 64, 64, 512, 1.36f, 0.486f, 0.431f, 0.621f, 5.32f, 0.813f, 1.41f, 0.159f},
+                           {kI8Tile32x64, 32, 64, 256, 1.71f, 0.171f, 0.805f, 0.842f, 4.44f, 0.32f, 0.0261f, 0.349f}};
 
 // Streams, bn x bm: start + each n + blocks (per_run + more n), n tiles.  Dot
 // products, bn columns (four waves) x 1: the same in runs of K that a wave has
@@ -45,13 +48,13 @@ struct StreamCost {
   float start, each, per_run, more, memory;
 };
 constexpr int kAny = 1 << 30;
-const StreamCost kStreams[] = {{kI8Stream16, 16, 16, 128, 64, 20, 512, 3.03f, 0.00138f, 0.0500f, 0.00017f, 4.0f},
-                               {kI8Stream16Deep, 16, 16, 128, 64, 20, 512, 2.97f, 0.00266f, 0.0373f, 0.00016f, 3.9f},
-                               {kI8Stream32, 32, 16, 128, 64, 40, kAny, 2.94f, 0.00233f, 0.127f, 0.00017f, 4.75f},
-                               {kI8Stream16x32, 16, 32, 128, 200, 40, kAny, 3.20f, 0.00158f, 0.0545f, 0.00026f, 3.4f},
-                               {kI8Dot2, 8, 1, 8192, 4, 1, kAny, 2.20f, 0.00161f, 0.744f, 0.00172f, 3.85f},
-                               {kI8Dot4, 16, 1, 4096, 4, 1, kAny, 1.70f, 0.f, 1.21f, 0.00326f, 5.7f},
-                               {kI8Dot8, 32, 1, 2048, 4, 1, kAny, 2.10f, 0.f, 0.94f, 0.00309f, 5.7f}};
+const StreamCost kStreams[] = {{kI8Stream16, 16, 16, 128, 128, 20, 512, 3.02f, 0.00144f, 0.0511f, 0.000152f, 4.58f},
+                               {kI8Stream16Deep, 16, 16, 128, 128, 20, 512, 3.05f, 0.00251f, 0.0295f, 0.000175f, 4.75f},
+                               {kI8Stream32, 32, 16, 128, 128, 64, kAny, 2.91f, 0.00169f, 0.172f, 0.000202f, 5.31f},
+                               {kI8Stream16x32, 16, 32, 128, 512, 64, kAny, 3.21f, 0.00143f, 0.0537f, 0.000282f, 2.28f},
+                               {kI8Dot2, 8, 1, 8192, 4, 1, kAny, 3.03f, 0.002f, 0.276f, 0.00252f, 7.97f},
+                               {kI8Dot4, 16, 1, 4096, 4, 1, kAny, 1.33f, 0.0000340f, 1.14f, 0.00329f, 7.62f},
+                               {kI8Dot8, 32, 1, 2048, 4, 1, kAny, 1.91f, 0.f, 1.01f, 0.00326f, 7.66f}};
 
 const char* const kNames[] = {"dot 2", "dot 4", "dot 8", "stream 16x16", "stream 16x16 deep", "stream 32x16", "stream 16x32", "tile 256x256",
                               "tile 256x128", "tile 128x128", "tile 128x64", "tile 64x64", "tile 32x64"};
@@ -86,7 +89,8 @@ Int8Form int8_form(bool grouped, int T, int E, int N, int K) {
     const float n = up((float)N, (float)f.bn) * (float)groups * m, at = (float)f.at_once;
     const float whole = up(n, at) - 1.f, full = (n - whole * at) / at;
     const float start = f.start + (grouped ? f.look : 0.f), step = blocks * f.per_block * (K % 128 ? 1.f + f.split : 1.f);
-    take(f.form, 2.f + whole * (start + step) + start + step * (f.few + (1.f - f.few) * full) + f.end * fminf(1.f, n / at), f.memory);
+    const float part = full < 0.5f ? f.few + (f.half - f.few) * 2.f * full : f.half + (1.f - f.half) * (2.f * full - 1.f);
+    take(f.form, 2.f + whole * (start + step) + start + step * part + f.end * fminf(1.f, n / at), f.memory);
   }
   return best;
 }
