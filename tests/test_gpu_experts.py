@@ -77,7 +77,8 @@ def test_route(mode, half, M, E, top):
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("M,E,top,G,keep", [(20, 16, 4, 2, 1), (9, 16, 4, 16, 5), (30, 256, 8, 8, 4), (70, 160, 6, 8, 3), (12, 60, 5, 4, 2),
                                             (11, 60, 5, 3, 2), (13, 60, 8, 12, 5), (66, 320, 8, 16, 4), (8, 1024, 16, 64, 9), (10, 96, 4, 32, 7),
-                                            (21, 1000, 20, 8, 3), (6, 490, 8, 7, 7), (5, 63, 2, 63, 9), (4, 64, 3, 64, 3), (300, 36, 6, 6, 3)])
+                                            (21, 1000, 20, 8, 3), (6, 490, 8, 7, 7), (5, 63, 2, 63, 9), (4, 64, 3, 64, 3), (300, 36, 6, 6, 3),
+                                                     (100, 490, 8, 7, 4), (1100, 245, 4, 5, 2), (900, 64, 6, 8, 3), (1024, 300, 5, 4, 3)])
 def test_route_groups(group_score, bias, M, E, top, G, keep):
     case(f"route groups {group_score} bias={bias} {M} of {E} top {top} {keep} of {G}")
     b = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)) if bias else None
