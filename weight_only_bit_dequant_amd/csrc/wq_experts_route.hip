@@ -696,9 +696,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   if (a.M == 0) return launch(k_no_tokens, dim3(1), 256, 0, s, a.offsets, a.E + 1);
   const bool wide = a.bias || a.pairs;
   Stretches st = stretches(a.M);
-  // one launch of one workgroup where that takes no longer than two: 64 tokens of 128 experts 8.4 us; by biased scores, 64
-  // of 256 in groups, it took 20
-  if (a.M > kFewSpan && a.M <= kSpan && !wide) st = {kSpan, 1, 1};
+  // one launch of one workgroup where that takes no longer than two: 64 tokens of 128 experts 8.9 us, 9.3 in two, 17 8.4 and
+  // 9.0; 64 of 256 11.3 and 9.8, of 1024 34 and 12; by biased scores, 64 of 256 in groups 20 and 11
+  if (a.M > kFewSpan && a.M <= kSpan && a.E <= 128 && !wide) st = {kSpan, 1, 1};
   const bool on_lanes = (a.groups & (a.groups - 1)) == 0;
   auto fits = [&](int lanes, int regs, Layout& at) {
     if (a.top > lanes || (on_lanes && a.groups > lanes)) return false;
