@@ -58,8 +58,9 @@ enum {
  *              expert in their order; not written from offsets[E] on
  *   places   : int32 [M][top]; t of each choice, -1 where there is none
  *   workspace: wq_experts_route_workspace(M, E) bytes, 4-byte aligned (NULL where
- *              that is 0), no contents kept between calls; calls that may run
- *              concurrently need different ones
+ *              that is 0), no contents kept between calls; one for M tokens and E
+ *              experts serves fewer of either, calls that may run concurrently need
+ *              different ones
  * 1 <= E <= 1024, 1 <= top <= min(E, 32), 1 <= keep <= groups <= 64, M * top < 2^30
  * (WQ_EUNSUPPORTED above).  With M == 0 the offsets are written, all zero.
  * The outputs overlap neither each other nor the inputs.

@@ -311,6 +311,12 @@ def test_workspace():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     with pytest.raises(ValueError):
         experts.route(l, 4, workspace=dirty[: need - 4])
+    # one for the largest batch serves smaller ones
+    l = logits_of(5000, 60, 4).to(DEV)
+    kept = torch.full((experts.workspace_bytes(5000, 60),), 255, dtype=torch.uint8, device=DEV)
+    for M in (5000, 4096, 1025, 1024, 700, 17, 3):
+        want, got = experts.route(l[:M], 4), experts.route(l[:M], 4, workspace=kept)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 def test_refusals():

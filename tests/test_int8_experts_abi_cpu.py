@@ -162,6 +162,10 @@ def test_route_workspace():
     size = experts._lib().wq_experts_route_workspace
     assert size(0, 8) == size(-5, 8) == size(16, 8) == size(1000, 0) == size(1000, 2000) == size(1 << 40, 8) == 0
     assert size(64 * 256, 8) == 256 * 8 * 2
+    # what serves many tokens and experts serves fewer
+    sizes = [size(M, 60) for M in (*range(1, 5000), 16384, 16385, 65536, 65537, 1 << 20, 1 << 24, 1 << 25, 1 << 29)]
+    assert sizes == sorted(sizes)
+    assert all(size(700, E) <= size(700, E + 1) for E in range(1, 1024))
     for M in (65, 1000, 16384, 16385, 100000, 1 << 24):
         assert 0 < size(M, 1024) <= 257 * 1024 * 2
 

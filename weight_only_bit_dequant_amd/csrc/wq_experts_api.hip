@@ -12,7 +12,9 @@ extern "C" {
 
 size_t wq_experts_route_workspace(int64_t M, int64_t E) {
   if (M <= wq::kFewSpan || E <= 0 || M > kMaxDim || E > WQ_MAX_EXPERTS) return 0;
-  return (size_t)wq::stretches(M).count * (size_t)wq::counts_pitch((int)E) * sizeof(uint16_t);
+  // no less than fewer tokens need, which have more stretches up to a point
+  const int few = wq::stretches(M < wq::kWaves * wq::kMaxStretches ? M : wq::kWaves * wq::kMaxStretches).count, count = wq::stretches(M).count;
+  return (size_t)(count > few ? count : few) * (size_t)wq::counts_pitch((int)E) * sizeof(uint16_t);
 }
 
 wq_status wq_experts_route(const void* logits, int logit_bits, int64_t ld, int64_t M, int64_t E, int64_t top, int score,

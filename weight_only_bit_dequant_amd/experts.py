@@ -68,7 +68,7 @@ def buffers(M, E, top, device):
 
 
 def workspace_bytes(M, E):
-    """Bytes of the workspace that ``route`` needs for M tokens and E experts (0: none)."""
+    """Bytes of the workspace that ``route`` needs for M tokens and E experts, or fewer of either (0: none)."""
     return _lib().wq_experts_route_workspace(M, E)
 
 
