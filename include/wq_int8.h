@@ -8,7 +8,7 @@
  * The quantizer, for a row of fp32 values y:
  *   s    = max(amax / 127, 2^-126), amax = max |y|, one IEEE fp32 division
  *   code = y / s to the nearest whole number, ties to even; the fp32 quotient is
- *          within one ulp of IEEE division's (two for a gated row)
+ *          within one ulp of IEEE division's
  * The floor 2^-126 keeps 1 / s finite: a row of zeros has that scale and codes 0.
  * A row that holds a NaN or an infinity has the scale NaN and codes 0: no finite
  * value is made up for it, and all that is computed from it is NaN.
@@ -46,9 +46,9 @@ wq_status wq_int8_quantize_act(const void* X, int64_t ldx, int64_t M, int64_t K,
  * Gated activation with a quantized result: GU holds rows of 2 K bf16 values
  * (row m at GU + m * ldg elements; ldg >= 2 K, ldg % 8 == 0), gate first;
  *   y[k] = silu(GU[m][k]) * GU[m][K + k],  silu(g) = g / (1 + exp(-g))
- * in fp32.  silu is within 2^-16 of itself (some 2^-21 where it is not small), -0
- * for finite g < -87.3, g for infinite g > 0 and NaN for g = -infinity, as the
- * formula has them.  Xq/Xs receive y quantized.
+ * in fp32, y within 10 * 2^-24 of itself, as far as exp(-g) is a number in fp32;
+ * beyond (g < -88.72) it is -0, as the fp32 formula has it.  Infinite gates spoil
+ * their row: y is an infinity or a NaN.  Xq/Xs receive y quantized.
  */
 wq_status wq_int8_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int64_t K, void* Xq, float* Xs,
                                     void* stream);

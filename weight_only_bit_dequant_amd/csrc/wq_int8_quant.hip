@@ -41,8 +41,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part, int wave
 }
 
 struct RowScale {
-  float s, inv;
-  bool bad;  // an infinity or a NaN among the row
+  float s, inv, rest;  // inv + rest = 1 / s to some 48 bits
+  bool bad;            // an infinity or a NaN among the row
 };
 __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   RowScale r;
@@ -50,26 +50,27 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   r.s = bitsf(r.bad ? 0 : amax_bits) / 127.0f;
   r.s = r.s < kTiny ? kTiny : r.s;
   r.inv = 1.0f / r.s;
+  r.rest = __builtin_fmaf(-r.s, r.inv, 1.0f) * r.inv;
   return r;
 }
 
-// Codes of y / s.  EXACT: the quotient as y * (1 / s) and one correction by its
-// remainder: IEEE division's result but for rare last bits, at a third of its
-// instructions.  (Of bf16 rows a thousandth of the quotients are within an ulp of a
-// tie: y * (1 / s) alone takes two in three of those to the other side.)  Otherwise,
-// where y itself was rounded, the product.  Adding 1.5 * 2^23 rounds to a whole
-// number, ties to even, whose low byte is the sum's.  |y / s| < 127.5 by the choice
-// of s.
-template <bool EXACT>
+// Codes of y / s, the quotient IEEE division's but for rare last bits, at a third of its
+// instructions: y * (1 / s) and one correction by its remainder, or, of gated rows, y times
+// 1 / s in two parts, one instruction less (4096 x 5632: 20.4 us, 21.0).  (Of bf16 rows a
+// thousandth of the quotients are within an ulp of a tie: y * (1 / s) alone takes two in three
+// of those to the other side.  Of 23 million gated values 11 have another code by it than the
+// fp32 formula gives, 3 so; it saves 0.9 us.)  Adding 1.5 * 2^23 rounds to a whole number,
+// ties to even, whose low byte is the sum's.  |y / s| < 127.5 by the choice of s.
+template <bool GATE>
 __device__ __forceinline__ u32x2 codes8(const F8& y, const RowScale& r) {
   uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if constexpr (EXACT) {
+    if constexpr (GATE) {
+      b[i] = fbits(__builtin_fmaf(y.v[i], r.inv, y.v[i] * r.rest) + 12582912.0f);
+    } else {
       const float v = y.v[i] * r.inv;
       b[i] = fbits(__builtin_fmaf(__builtin_fmaf(-v, r.s, y.v[i]), r.inv, v) + 12582912.0f);
-    } else {
-      b[i] = fbits(__builtin_fmaf(y.v[i], r.inv, 12582912.0f));
     }
   }
   u32x2 w;
@@ -82,20 +83,27 @@ __device__ __forceinline__ u32x2 codes8(const F8& y, const RowScale& r) {
   return w;
 }
 
-// silu(g) u = g / (1 + exp(-g)) u on the hardware's 2^x and reciprocal (an ulp
-// each).  The exponent's one rounding makes exp(-g) off by |g| 2^-24 of itself: what
-// counts of that is below 2^-21 where silu is more than a millionth of its size
-// elsewhere, far below a code's step.  Where exp(-g) passes 2^126 (g < -87.3) the
-// result is -0; infinities and NaN are as the formula has them.  Six instructions; one
-// more exact by two bits takes sixteen and is this kernel's time (4096 x 5632: 30 us).
+// silu(g) u = g / (1 + exp(-g)) u of a bf16 gate, within 10 2^-24 of itself (all 65536 gates: 2.3 ulp of
+// silu at most, 0.075 on average; fp32's exp, sum and quotient 1.75 and 0.063).
+//   exp(-g) = 2^(-g L) (1 - g C), L = log2 e cut to 16 bits, so that its product with the 8 bits of g is exact
+//     and 2^x gets its argument unrounded; C = (log2 e - L) ln 2, and (g C)^2 / 2, less than 1.6 2^-24, is left out
+//   the quotient is g' / d' with g' = 2^-8 g, d' = 2^-8 (1 + exp(-g)), on the hardware's reciprocal (an ulp): it
+//     reads reciprocals below 2^-126 as 0, and d' stays below 2^120
+// Below -88.72 exp(-g) leaves fp32 and the result is -0, as the formula has it there.  Infinite gates may give
+// NaN for an infinity: their row holds neither codes nor a scale.  4096 x 5632 20.4 us; with one rounding of the
+// exponent (up to 55 ulp off) 18.8, with the quotient corrected by its remainder (1 code in 23 million differs
+// from the formula's, 3 so) 21.6, by expf and division 32.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  const float d = 1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f);
-  return g * __builtin_amdgcn_rcpf(d) * u;
+  constexpr float L = 369.328125f, C = 0.00125145476f;  // 2^8 times the constants above
+  const float n = g * 0.00390625f;
+  const float p = __builtin_amdgcn_exp2f(n * -L);
+  const float e = __builtin_fmaf(p, n * -C, p);
+  return n * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.00390625f, 0.00390625f)) * u;
 }
 
 __device__ __forceinline__ float stored(const RowScale& r) { return r.bad ? __builtin_nanf("") : r.s; }
 
-// Bound by memory: 8192 x 8192 in 29.4 us (6.8 TB/s), gated 60.5 (5.5 TB/s), 4096 x 5632 gated 19.2 (6.0 TB/s); a few
+// Bound by memory: 8192 x 8192 in 29.4 us (6.8 TB/s), gated 61.6 (5.45 TB/s), 4096 x 5632 gated 20.5 (5.6 TB/s); a few
 // rows by the launch and one trip to memory, 2.6 us.
 template <bool GATE, int WPR, int CPT>
 __global__ __launch_bounds__(rows_per_group<WPR>() * WPR * 64) void k_int8_rows(const uint16_t* X, int64_t ldx, int M,
@@ -135,7 +143,7 @@ __global__ __launch_bounds__(rows_per_group<WPR>() * WPR * 64) void k_int8_rows(
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     const uint32_t c = c0 + 64u * WPR * j;
-    if (live && c * 8u < (uint32_t)K) *reinterpret_cast<u32x2*>(Xq + m * K + c * 8u) = codes8<!GATE>(y[j], r);
+    if (live && c * 8u < (uint32_t)K) *reinterpret_cast<u32x2*>(Xq + m * K + c * 8u) = codes8<GATE>(y[j], r);
   }
   if (live && c0 == 0) Xs[m] = stored(r);
 }
@@ -160,7 +168,7 @@ __global__ __launch_bounds__(1024) void k_int8_long_rows(const uint16_t* X, int6
   uint32_t amax = 0;
   for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) amax = max(amax, absmax8(at(k)));
   const RowScale r = row_scale(row_max<16>(amax, part, wave, lane));
-  for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) *reinterpret_cast<u32x2*>(Xq + m * K + k) = codes8<!GATE>(at(k), r);
+  for (int k = 8 * (int)threadIdx.x; k < K; k += 8192) *reinterpret_cast<u32x2*>(Xq + m * K + k) = codes8<GATE>(at(k), r);
   if (threadIdx.x == 0) Xs[m] = stored(r);
 }
 
