@@ -43,6 +43,15 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
 }
 
+// An output before its rounding to bf16, each operation rounded by itself: joined into a multiply-add, as the compiler does
+// where it may, the bias would meet an unrounded product in some forms and not in others, and a row's bits go by the number
+// of rows beside it.  Without a bias kNoBias is added, which leaves every value as it is, -0 too.
+constexpr uint16_t kNoBias = 0x8000;  // -0
+__device__ __forceinline__ float output(int sum, float xs, float ws, float bias) {
+#pragma clang fp contract(off)
+  return (float)sum * xs * ws + bias;
+}
+
 // ---------------------------------------------------------------- single rows: dot products
 // A wave owns C columns of one row; its lanes split K, 16 codes of every 1024
 // each, so that one instruction reads 1 KiB of one weight row, and multiply by
@@ -77,7 +86,7 @@ __global__ __launch_bounds__(256) void k_int8_dot(Int8GemmArgs a, int gx, int gy
   // lane i's column at the end
   const int n = n0 + min(lane, cols - 1);
   const float xs = has ? a.Xs[src] : 0.f, ws = a.Ws[(int64_t)t.e * N + n];
-  const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f;
+  const float bias = bf16_to_f32(a.bias ? a.bias[n] : kNoBias);
 
   constexpr int U = kAhead / C;  // KiB of a row at a time
   int acc[C] = {};
@@ -103,9 +112,7 @@ __global__ __launch_bounds__(256) void k_int8_dot(Int8GemmArgs a, int gx, int gy
     sum = lane == i ? s : sum;
   }
   if (lane < cols) {
-    float y = (float)sum * xs * ws;
-    if (a.bias) y += bias;
-    a.Y[(int64_t)t.t0 * N + n] = f32_to_bf16(y);
+    a.Y[(int64_t)t.t0 * N + n] = f32_to_bf16(output(sum, xs, ws, bias));
   }
 }
 
@@ -234,8 +241,7 @@ __global__ __launch_bounds__(W * 64) void k_int8_stream(Int8GemmArgs a, int gx, 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int nr = min(n + r, N - 1);
-      y[r] = (float)s[r] * xs * a.Ws[(int64_t)t.e * N + nr];
-      if (a.bias) y[r] += bf16_to_f32(a.bias[nr]);
+      y[r] = output(s[r], xs, a.Ws[(int64_t)t.e * N + nr], bf16_to_f32(a.bias ? a.bias[nr] : kNoBias));
     }
     uint16_t* p = a.Y + (int64_t)m * N + n;
     if ((N & 3) == 0) {
@@ -371,7 +377,7 @@ __device__ __forceinline__ void tile(const Int8GemmArgs& a, const RowTile t, con
   for (int u = 0; u < PER; ++u) {
     const int i = (int)threadIdx.x + u * T::THREADS, n = min(n0 + (i < BN ? i : i - BN), N - 1);
     raw[u] = *(i < 2 * BN ? a.Ws + (int64_t)t.e * N + n : a.Xs + min(src[u], (uint32_t)a.M - 1));
-    rawb[u] = a.bias ? a.bias[n] : 0u;
+    rawb[u] = a.bias ? a.bias[n] : kNoBias;
   }
 #pragma unroll
   for (int i = 2; i < U - 2; ++i)
@@ -503,7 +509,7 @@ __device__ __forceinline__ void tile(const Int8GemmArgs& a, const RowTile t, con
         const f32x4 w = *reinterpret_cast<const f32x4*>(ws + n + 4 * half), b = *reinterpret_cast<const f32x4*>(bs + n + 4 * half);
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = (float)s[e] * xs[r] * w[e] + b[e];
+        for (int e = 0; e < 4; ++e) y[e] = output(s[e], xs[r], w[e], b[e]);
         v[2 * half] = pack(y[0], y[1]);
         v[2 * half + 1] = pack(y[2], y[3]);
       }
@@ -526,7 +532,7 @@ __device__ __forceinline__ void tile(const Int8GemmArgs& a, const RowTile t, con
         for (int j = 0; j < TM; ++j) {
           float y[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) y[r] = (float)acc[i][j][4 * q + r] * xm[j] * w[r] + b[r];
+          for (int r = 0; r < 4; ++r) y[r] = output(acc[i][j][4 * q + r], xm[j], w[r], b[r]);
           *reinterpret_cast<u32x2*>(et + (32 * j + c) * T::PITCH + (32 * i + 8 * q + 4 * h) * 2) =
               u32x2{pack(y[0], y[1]), pack(y[2], y[3])};
         }
