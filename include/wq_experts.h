@@ -44,9 +44,10 @@ enum {
  *   Ties go to the lowest index, of experts and of groups; a NaN is larger than
  *   any number, and equal to any NaN.  A softmax over a NaN or +infinity is NaN
  *   throughout.
- *   Scores that a bias or pairs compare, and weights' ratios, are held in fp64;
- *   a softmax sum that only weights need in fp32.  Choices of scores may
- *   count as equal where they differ by less than 2^-43 of their size.
+ *   Scores that a bias or pairs compare, and weights' ratios, are held in fp64; a
+ *   softmax sum that only weights need in fp32.  Choices are compared in all
+ *   their bits, whatever M.  (A softmax's scores are within 2^-48 of themselves:
+ *   the order of its sum goes by M and E.)
  *
  *   logits   : fp32 (logit_bits 32) or bf16 (16), row m at logits + m * ld elements, E <= ld < 2^22
  *   bias     : fp32 [E] or NULL

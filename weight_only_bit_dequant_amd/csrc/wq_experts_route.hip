@@ -78,7 +78,8 @@ struct Wide {
 };
 
 // Choices with their expert's number in the low BITS bits (the lowest expert the largest): no two experts' are equal, and
-// the number comes with the choice through maxima and sorting.  That takes 2^-43 or less of a choice: nearer ones are equal.
+// the number comes with the choice through maxima and sorting.  Choices that differ in those bits alone are told apart
+// afterwards (`unsure` below).
 template <int BITS>
 struct Numbered {
   static constexpr uint32_t MASK = (1u << BITS) - 1;
@@ -220,10 +221,15 @@ __device__ __forceinline__ T sum_over(T v, int n) {
   return over(v, n, [](T a, T b) { return a + b; });
 }
 
+// What makes a group's value, of its n lanes' two largest: the two largest of all, or the largest and none.
+template <class K>
+__device__ __forceinline__ Two<K> best_over(Two<K> t, int n, bool pairs) {
+  if (!pairs) return {max_over<K>(t.a, n), K::kNot};
+  return over(t, n, [](Two<K> x, Two<K> y) { return Two<K>{K::max(x.a, y.a), K::max(K::min(x.a, y.a), K::max(x.b, y.b))}; });
+}
 template <class K>
 __device__ __forceinline__ typename K::T group_value(Two<K> t, int n, bool pairs) {
-  if (!pairs) return max_over<K>(t.a, n);
-  const Two<K> r = over(t, n, [](Two<K> x, Two<K> y) { return Two<K>{K::max(x.a, y.a), K::max(K::min(x.a, y.a), K::max(x.b, y.b))}; });
+  const Two<K> r = best_over<K>(t, n, pairs);
   return K::sum(r.a, r.b);
 }
 
@@ -356,10 +362,38 @@ __device__ __forceinline__ int better_groups(typename K::T v, int group, int lan
   return better;
 }
 
+// Of group values known to lie in [lo, hi]: how many other groups are surely better, and how many may be, or be equal.
+template <int L>
+__device__ __forceinline__ void rank_groups(double lo, double hi, int lanes, int groups, int lane, int& surely, int& maybe) {
+  surely = maybe = 0;
+  auto against = [&](double olo, double ohi) {
+    surely += olo > hi;
+    maybe += ohi >= lo;
+  };
+  if constexpr (L == 16) {
+    unroll16([&](auto by) {
+      constexpr int BY = decltype(by)::value;
+      if (BY % lanes) return;  // (uniform)
+      against(dpp<0x120 + BY>(lo), dpp<0x120 + BY>(hi));
+    });
+  } else {
+    for (int g = 0; g < groups; ++g) against(__shfl(lo, lane / L * L + g * lanes), __shfl(hi, lane / L * L + g * lanes));
+    --maybe;  // (itself)
+  }
+}
+
 // D = 0: each pick looks through all choices of the lanes.  D > 0, of fp64 choices: each lane orders its D largest (as many
-// as are picked, or all it has) first, and a pick is the largest of the lanes' first ones.  16384 of 256 experts by biased
-// scores: 29.4 -> 25.1 us, in groups 31.7 -> 27.1, of 512 53 -> 40; by logits, whose keys take half the registers, 20.2 -> 19.5
-// for 8 picks and 26.6 -> 31.3 for 16.
+// as are picked, or all it has) first, and a pick is the largest of the lanes' first ones.  The numbers in the choices' low
+// bits may have put near ones in the wrong order there; where they can have, the wave does its tokens again as D = 0 does:
+//   a group's value lies within 2^-42 of the size of its choices from what they are without those bits; it is unsure
+//     whether a group stays if it depends on where (a relative bound above 2^(BITS - 52), and 2^-1000 for subnormal ones)
+//   picks go on for as long as the next is equal to the last in all other bits, so that all such are seen; neighbours
+//     that are equal so have to have the same logit and bias: then they are equal, and the lowest index is first
+//   a lane whose D ordered choices are all picked may have had more of them
+// 16384 of 256 experts by biased scores: 25.0 us, 29.4 with D = 0, in groups 26.7 and 31.7; of 512 43 and 53.  The checks are
+// 0.2 to 0.8 us of it (of 512 3, for registers).  Groups of the same value at the border are done again: with bf16 logits and
+// no bias, or few values of one, 31 us in pairs, 38 by the largest.  By logits, whose keys take half the registers, ordering
+// makes 20.2 us 19.5 for 8 picks and 26.6 31.3 for 16.
 template <int L, int R, int D, class K, bool LOOSE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int span, int passes) {
   typedef typename K::T T;
@@ -398,144 +432,190 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, Layout at, int s
       const int t = sub + slot;
       const int64_t m = m0 + t;
       const bool live = t < tokens && (!a.valid || a.valid[m]);
-      T key[R];
-      uint32_t biggest = 0;  // key of the row's largest logit
-      double sum = 0.0;
+      uint32_t biggest;  // key of the row's largest logit
+      double sum;
       float peak;
-      {
-        float logit[R];
-        load_run<R>(rows, ((uint32_t)t * (uint32_t)a.ld + (uint32_t)first) * (a.half ? 2u : 4u), live ? mine : 0, a.half, at.whole,
-                    WIDE && a.sigmoid && live ? 0.f : -__builtin_inff(), logit);
-        if (!a.sigmoid || !WIDE) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t k = Narrow::of(logit[r]);
-            if constexpr (!WIDE) key[r] = k;
-            biggest = max(biggest, k);
-          }
-          biggest = max_over<Narrow>(biggest, L);
-        }
-        peak = Narrow::logit(biggest);
-        if constexpr (WIDE) {
-          // choices of numbers; infinities and NaN, if the wave has any, after that (a logit of +infinity has the score 1)
-          constexpr int kNaNs = 0x003, kBelow = 0x004, kAbove = 0x200;
-          bool odd;
-          if (a.sigmoid) {
-            odd = false;
+      int pick;  // of lane j: the j-th largest choice
+      float x;   // its logit
+      for (bool whole = D == 0;; whole = true) {  // whether choices are compared in all their bits
+        T key[R];
+        biggest = 0, sum = 0.0;
+        // (as if new each time: kept through the loop, what comes of them takes registers that are not there)
+        int token = t, from = first, count = live ? mine : 0;
+        if constexpr (D > 0) asm volatile("" : "+v"(token), "+v"(from), "+v"(count));
+        {
+          float logit[R];
+          load_run<R>(rows, ((uint32_t)token * (uint32_t)a.ld + (uint32_t)from) * (a.half ? 2u : 4u), count, a.half, at.whole,
+                      WIDE && a.sigmoid && live ? 0.f : -__builtin_inff(), logit);
+          if (!a.sigmoid || !WIDE) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              key[r] = sigmoid_of_number(logit[r]) + bias[r];
-              odd |= __builtin_amdgcn_classf(logit[r], kNaNs | kBelow);
-              if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (16 at once would not fit the registers)
+              const uint32_t k = Narrow::of(logit[r]);
+              if constexpr (!WIDE) key[r] = k;
+              biggest = max(biggest, k);
             }
-          } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              sum += key[r] = below_finite_peak(logit[r], peak);
-              if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-            }
-            sum = sum_over(sum, L);
-            const double part = 1.0 / sum;
-            odd = __builtin_amdgcn_classf(peak, kNaNs | kBelow | kAbove);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              key[r] = __builtin_fma(key[r], part, bias[r]);
-              odd |= __builtin_amdgcn_classf(logit[r], kBelow);
-            }
+            biggest = max_over<Narrow>(biggest, L);
           }
-          if (__any(odd)) {
-            const bool all = !a.sigmoid && __builtin_amdgcn_classf(peak, kNaNs | kAbove);
+          peak = Narrow::logit(biggest);
+          if constexpr (WIDE) {
+            // choices of numbers; infinities and NaN, if the wave has any, after that (a logit of +infinity has the score 1)
+            constexpr int kNaNs = 0x003, kBelow = 0x004, kAbove = 0x200;
+            bool odd;
+            if (a.sigmoid) {
+              odd = false;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-              key[r] = either(logit[r] == -__builtin_inff(), K::kNot, either(all || logit[r] != logit[r], K::kNaN, key[r]));
-          }
-        } else if (!a.sigmoid && !a.renormalize) {
-          float each = 0.f;
+              for (int r = 0; r < R; ++r) {
+                key[r] = sigmoid_of_number(logit[r]) + bias[r];
+                odd |= __builtin_amdgcn_classf(logit[r], kNaNs | kBelow);
+                if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (16 at once would not fit the registers)
+              }
+            } else {
 #pragma unroll
-          for (int r = 0; r < R; ++r) each += logit[r] == -__builtin_inff() ? 0.f : expf(logit[r] - peak);
-          sum = sum_over(each, L);
-        }
-      }
-
-      int pick = -1;  // of lane j: the j-th largest choice
-      float x = 0.f;  // its logit
-      if constexpr (D > 0) {
-        typedef Numbered<__builtin_ctz(L * R)> N;
+              for (int r = 0; r < R; ++r) {
+                sum += key[r] = below_finite_peak(logit[r], peak);
+                if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+              }
+              sum = sum_over(sum, L);
+              const double part = 1.0 / sum;
+              odd = __builtin_amdgcn_classf(peak, kNaNs | kBelow | kAbove);
 #pragma unroll
-        for (int r = 0; r < R; ++r) key[r] = N::of(key[r], first + r);
-        largest<R, D>(key);
-        if (a.groups > 1) {
-          const double of_group = group_value<K>(Two<K>{N::choice(key[0]), N::choice(key[1])}, at.lanes, a.pairs);
-          if (better_groups<L, K>(of_group, group, at.lanes, a.groups, tid & 63) >= a.keep) {
-#pragma unroll
-            for (int r = 0; r < D; ++r) key[r] = K::kNot;
-          }
-        }
-        double own = K::kNot;
-        for (int j = 0; j < top; ++j) {
-          const double best = max_over<K>(key[0], L);
-          const bool taken = key[0] == best;
-#pragma unroll
-          for (int r = 0; r < D; ++r) key[r] = either(taken, r + 1 < D ? key[r + 1] : K::kNot, key[r]);
-          own = l == j ? best : own;
-        }
-        if (N::choice(own) != K::kNot) pick = N::expert(own);
-      } else {
-        if (a.groups > 1) {
-          if constexpr (!LOOSE) {
-            Two<K> two{K::kNot, K::kNot};
-#pragma unroll
-            for (int r = 0; r < R; ++r) two.add(key[r]);
-            const T v = group_value<K>(two, at.lanes, a.pairs);
-            if (better_groups<L, K>(v, group, at.lanes, a.groups, tid & 63) >= a.keep) {
-#pragma unroll
-              for (int r = 0; r < R; ++r) key[r] = K::kNot;
+              for (int r = 0; r < R; ++r) {
+                key[r] = __builtin_fma(key[r], part, bias[r]);
+                odd |= __builtin_amdgcn_classf(logit[r], kBelow);
+              }
             }
-          } else {
-            T* value = reinterpret_cast<T*>(loose) + slot * a.groups;
-            const int size = E / a.groups;
-            for (int g = 0; g < a.groups; ++g) {
-              Two<K> t2{K::kNot, K::kNot};
+            if (__any(odd)) {
+              const bool all = !a.sigmoid && __builtin_amdgcn_classf(peak, kNaNs | kAbove);
 #pragma unroll
               for (int r = 0; r < R; ++r)
-                if ((first + r) / size == g) t2.add(key[r]);
-              const T v = group_value<K>(t2, L, a.pairs);
-              if (l == 0) value[g] = v;
+                key[r] = either(logit[r] == -__builtin_inff(), K::kNot, either(all || logit[r] != logit[r], K::kNaN, key[r]));
             }
-            __syncthreads();
+          } else if (!a.sigmoid && !a.renormalize) {
+            float each = 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if (r >= mine) continue;
-              const int own = (first + r) / size;
-              const T v = value[own];
-              int better = 0;
-              for (int g = 0; g < a.groups; ++g) better += value[g] > v || (value[g] == v && g < own);
-              if (better >= a.keep) key[r] = K::kNot;
-            }
-            __syncthreads();
+            for (int r = 0; r < R; ++r) each += logit[r] == -__builtin_inff() ? 0.f : expf(logit[r] - peak);
+            sum = sum_over(each, L);
           }
         }
 
-        for (int j = 0; j < top; ++j) {
-          T best = key[0];
+        pick = -1, x = 0.f;
+        if constexpr (D > 0) {
+          if (!whole) {
+            typedef Numbered<__builtin_ctz(L * R)> N;
 #pragma unroll
-          for (int r = 1; r < R; ++r) best = K::max(best, key[r]);
-          best = max_over<K>(best, L);
-          uint32_t e = ~0u;  // the lowest expert of that key
+            for (int r = 0; r < R; ++r) key[r] = N::of(key[r], from + r);
+            largest<R, D>(key);
+            bool unsure = false;
+            if (a.groups > 1) {
+              const Two<K> best = best_over<K>(Two<K>{N::choice(key[0]), N::choice(key[1])}, at.lanes, a.pairs);
+              const double value = K::sum(best.a, best.b), size = __builtin_fabs(best.a) + (best.b == K::kNot ? 0.0 : __builtin_fabs(best.b));
+              const double off = __builtin_fma(size, 0x1p-42, 0x1p-1000);
+              int surely, maybe;
+              rank_groups<L>(value - off, value + off, at.lanes, a.groups, tid & 63, surely, maybe);
+              unsure = best.a != K::kNot && surely < a.keep && maybe >= a.keep;
+              if (maybe >= a.keep) {
 #pragma unroll
-          for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(first + r) : e;
-          if constexpr (L == 64) {
-            e = __builtin_amdgcn_readlane(e, __builtin_ctzll(__ballot(e != ~0u)));
-          } else {
-            e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+                for (int r = 0; r < D; ++r) key[r] = K::kNot;
+              }
+            }
+            const double held = key[D - 1];  // the least of this lane that can be picked
+            double own = K::kNot, last = K::kNot;
+            auto next = [&] {
+              const double best = max_over<K>(key[0], L);
+              const bool taken = key[0] == best;
+#pragma unroll
+              for (int r = 0; r < D; ++r) key[r] = either(taken, r + 1 < D ? key[r + 1] : K::kNot, key[r]);
+              return best;
+            };
+            for (int j = 0; j < top; ++j) {
+              last = next();
+              own = l == j ? last : own;
+            }
+            double least = last;
+            for (int j = top;; ++j) {
+              const double best = max_over<K>(key[0], L);
+              const bool more = N::choice(best) == N::choice(last) && N::choice(last) != K::kNot;
+              if (!__any(more)) break;
+              if (j == L) {
+                unsure |= more;
+                break;
+              }
+              next();
+              own = more && l == j ? best : own;
+              least = more ? best : least;
+            }
+            if constexpr (D < R) unsure |= N::choice(held) != K::kNot && held >= least;
+            const bool has = N::choice(own) != K::kNot;
+            const double before = L == 16 ? dpp<0x111>(own) : __shfl(own, (tid & 63) - 1);
+            const bool near = l > 0 && has && N::choice(own) == N::choice(before);
+            if (__any(near)) {
+              const float mine_l = has ? logit_at(a, m, N::expert(own)) : 0.f, mine_b = has && a.bias ? a.bias[N::expert(own)] : 0.f;
+              const float before_l = __shfl(mine_l, (tid & 63) - 1), before_b = __shfl(mine_b, (tid & 63) - 1);
+              unsure |= near && !(mine_l == before_l && mine_b == before_b);
+            }
+            if (__any(unsure)) continue;
+            if (l < top && has) pick = N::expert(own);
+            break;
           }
-          if (l == j && best != K::kNot) {
-            pick = (int)e;
-            if constexpr (!WIDE) x = Narrow::logit(best);
-          }
-#pragma unroll
-          for (int r = 0; r < R; ++r) key[r] = (uint32_t)(first + r) == e ? K::kNot : key[r];
         }
+        {
+          if (a.groups > 1) {
+            if constexpr (!LOOSE) {
+              Two<K> two{K::kNot, K::kNot};
+#pragma unroll
+              for (int r = 0; r < R; ++r) two.add(key[r]);
+              const T v = group_value<K>(two, at.lanes, a.pairs);
+              if (better_groups<L, K>(v, group, at.lanes, a.groups, tid & 63) >= a.keep) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) key[r] = K::kNot;
+              }
+            } else {
+              T* value = reinterpret_cast<T*>(loose) + slot * a.groups;
+              const int size = E / a.groups;
+              for (int g = 0; g < a.groups; ++g) {
+                Two<K> t2{K::kNot, K::kNot};
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                  if ((first + r) / size == g) t2.add(key[r]);
+                const T v = group_value<K>(t2, L, a.pairs);
+                if (l == 0) value[g] = v;
+              }
+              __syncthreads();
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                if (r >= mine) continue;
+                const int own = (first + r) / size;
+                const T v = value[own];
+                int better = 0;
+                for (int g = 0; g < a.groups; ++g) better += value[g] > v || (value[g] == v && g < own);
+                if (better >= a.keep) key[r] = K::kNot;
+              }
+              __syncthreads();
+            }
+          }
+
+          for (int j = 0; j < top; ++j) {
+            T best = key[0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) best = K::max(best, key[r]);
+            best = max_over<K>(best, L);
+            uint32_t e = ~0u;  // the lowest expert of that key
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) e = key[r] == best ? (uint32_t)(from + r) : e;
+            if constexpr (L == 64) {
+              e = __builtin_amdgcn_readlane(e, __builtin_ctzll(__ballot(e != ~0u)));
+            } else {
+              e = over(e, L, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+            }
+            if (l == j && best != K::kNot) {
+              pick = (int)e;
+              if constexpr (!WIDE) x = Narrow::logit(best);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) key[r] = (uint32_t)(from + r) == e ? K::kNot : key[r];
+          }
+        }
+        break;
       }
       if (WIDE && pick >= 0) x = logit_at(a, m, pick);
 
@@ -676,8 +756,9 @@ hipError_t launch_one(const RouteArgs& a, const Layout& at, const Stretches& st,
 }
 template <int L, int R, int THREADS, bool LOOSE = false>
 hipError_t route_launch(const RouteArgs& a, const Layout& at, const Stretches& st, bool wide, hipStream_t s) {
-  // (16 fp64 keys a lane do not fit the registers that 16 waves on a CU leave: 16384 of 256 experts 31.1 us, 28.9 with 8)
-  constexpr int WIDE_THREADS = R == 16 && L == 16 ? THREADS / 2 : THREADS;
+  // (16 fp64 keys a lane do not fit the registers that 16 waves on a CU leave: 16384 of 256 experts 31.1 us, 28.9 with 8; of
+  // 512 45.0, 43.2 with 8)
+  constexpr int WIDE_THREADS = R == 16 && L < 64 ? THREADS / 2 : THREADS;
   if (!wide) return launch_one<L, R, 0, Narrow, THREADS, LOOSE>(a, at, st, s);
   if constexpr (L < 64 && R >= 8) {
     if (a.top <= 4) return launch_one<L, R, 4, Wide, WIDE_THREADS, LOOSE>(a, at, st, s);
