@@ -44,10 +44,9 @@ enum {
  *   Ties go to the lowest index, of experts and of groups; a NaN is larger than
  *   any number, and equal to any NaN.  A softmax over a NaN or +infinity is NaN
  *   throughout.
- *   Scores that a bias or pairs compare, and weights' ratios, are held in fp64; a
- *   softmax sum that only weights need in fp32.  Choices are compared in all
- *   their bits, whatever M.  (A softmax's scores are within 2^-48 of themselves:
- *   the order of its sum goes by M and E.)
+ *   Scores, their sums and weights' ratios are held in fp64; a weight is rounded
+ *   once.  Choices are compared in all their bits, whatever M.  (A softmax's
+ *   scores are within 2^-48 of themselves: the order of its sum goes by M and E.)
  *
  *   logits   : fp32 (logit_bits 32) or bf16 (16), row m at logits + m * ld elements, E <= ld < 2^22
  *   bias     : fp32 [E] or NULL
