@@ -59,9 +59,7 @@ def test_linear_bits(form, M, N, K):
     check_linear(M, N, K)
 
 
-@pytest.mark.parametrize("form,counts,N,K,M,spare", F.GROUPED + F.GROUPED_SPLIT)
-def test_grouped_bits(form, counts, N, K, M, spare):
-    case(f"int8 grouped bits {form}: {sum(counts)} of {len(counts)} {N}x{K}")
+def check_grouped(counts, N, K, M):
     E = len(counts)
     off, rows = groups(counts, 7, M)
     T = int(off[-1])
@@ -73,6 +71,12 @@ def test_grouped_bits(form, counts, N, K, M, spare):
         if lo < hi:
             src = torch.arange(lo, hi, device=DEV) if rows is None else rows[lo:hi].long()
             same_bits(y[lo:hi], product(xq[src], xs[src], q["codes"][e], q["scales"][e]))
+
+
+@pytest.mark.parametrize("form,counts,N,K,M,spare", F.GROUPED + F.GROUPED_SPLIT)
+def test_grouped_bits(form, counts, N, K, M, spare):
+    case(f"int8 grouped bits {form}: {sum(counts)} of {len(counts)} {N}x{K}")
+    check_grouped(counts, N, K, M)
 
 
 @pytest.mark.parametrize("N,K", [(4096, 4096), (1200, 2064), (4200, 6240), (1096, 144), (8190, 528), (250, 1536)])
