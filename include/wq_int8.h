@@ -20,6 +20,8 @@
  * be 16-byte aligned (a bias 2-byte), the other pointers aligned to their type.
  * K % 16 == 0 everywhere (WQ_ESHAPE otherwise) and K < 2^17 (WQ_EUNSUPPORTED
  * otherwise): a sum of so many products of any two int8 codes fits an int32.
+ * The quantizers write nothing where there are no rows, or rows of no elements
+ * (K == 0), scales neither; the products refuse K == 0 (WQ_EUNSUPPORTED).
  * A call has fewer rows, or tiles, than a launch holds (some 2^22 to 2^26;
  * WQ_EUNSUPPORTED otherwise).
  */

@@ -24,6 +24,7 @@ PyObject* quant(Fn fn, int halves, PyObject* const* a, Py_ssize_t n) {  // (X, c
     const Rows x = rows(a[0], halves == 2 ? "GU" : "X");
     if (x.K % halves) throw Refused("GU must have an even number of columns (gate and up)");
     const int64_t K = x.K / halves;
+    if (K == 0 && x.M > 0) throw Refused(std::string(halves == 2 ? "GU" : "X") + " must have columns (rows of none would be left without scales)");
     void* xq = data(a[1], "codes", at::kChar, {x.M, K}, x.dev);
     void* xs = data(a[2], "scales", at::kFloat, {x.M}, x.dev);
     return on(x.dev, [&](void* s) { return fn(x.p, x.ld, x.M, K, xq, (float*)xs, s); });

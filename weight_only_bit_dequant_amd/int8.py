@@ -80,6 +80,7 @@ def quantize_weight(W):
     _need(isinstance(W, torch.Tensor) and W.dim() in (2, 3) and W.dtype is _BF16 and W.is_cuda and W.is_contiguous(),
           "W must be a contiguous bf16 tensor [N, K] or [E, N, K] on the GPU")
     N, K = W.shape[-2:]
+    _need(K > 0 or W.shape[:-1].numel() == 0, "W must have columns (rows of none would be left without scales)")
     E = 1 if W.dim() == 2 else W.shape[0]
     codes = torch.empty(W.shape, dtype=_I8, device=W.device)
     scales = torch.empty(W.shape[:-1], dtype=_F32, device=W.device)
