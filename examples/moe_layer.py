@@ -39,7 +39,7 @@ class MoELayer:
         """bf16 x, residual [M, hidden] -> (layer output, new residual)."""
         y = torch.empty_like(x)
         xq, xs, residual, _ = block.add_rmsnorm_quantize(x, self.gain, self.eps, residual=residual, y_out=y)
-        if self.ops is int8:
+        if self.ops is int8:  # (the norm has no form that leaves INT8 codes: its FP8 ones are not used)
             xq, xs = int8.quantize_act(y)
         r = self.route(y)
         gu = self.ops.grouped_linear(xq, xs, self.gate_up, r.offsets, rows=r.rows)

@@ -58,9 +58,10 @@ wq_status wq_int8_silu_mul_quantize(const void* GU, int64_t ldg, int64_t M, int6
 /*
  * Linear:
  *   Y[m][n] = bf16( float(sum_k Xq[m][k] Wq[n][k]) * Xs[m] * Ws[n] (+ bias[n]) )
- * The sum is exact (int32); from there on fp32: the sum is rounded once to 24
- * bits, multiplied by Xs, then by Ws, the bias is added, and the result rounded
- * once to bf16.  bias: bf16 [N] or NULL.  Any M and N.  No workspace.
+ * The sum is exact (int32); from there on fp32, each operation rounded by itself:
+ * the sum is rounded to 24 bits, multiplied by Xs, then by Ws, the bias is added,
+ * and the result rounded to bf16.  A row's bits do not go by the other rows or
+ * their number.  bias: bf16 [N] or NULL.  Any M and N.  No workspace.
  */
 wq_status wq_int8_linear(const void* Xq, const float* Xs, int64_t M, int64_t K, const void* Wq, const float* Ws,
                          const void* bias, int64_t N, void* Y, void* stream);

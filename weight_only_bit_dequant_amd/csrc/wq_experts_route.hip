@@ -20,7 +20,7 @@
 // take 20 us in the first launch, instructions: of some 1500 for four tokens a third
 // are the scores in fp64, a third the order in each lane and the eight picks (the next
 // tokens' logits fetched ahead, four scores' chains side by side: no change).  The second
-// takes 7 us, a few trips to memory.  By the logits alone the first takes 12 us.  One
+// takes 8 us, a few trips to memory.  By the logits alone the first takes 12 us.  One
 // token takes 4.9 us, 2.5 of them the launch, one trip to memory, and the picks one
 // after the other.
 #include <type_traits>

@@ -7,8 +7,12 @@
 // shapes and 290 grouped ones, random and powers of two (1 to 8192 rows, 256 to 8192
 // columns and K, weights from memory, graphs of back-to-back launches): over the
 // same shapes the chosen form takes 1.1 % more than the best one on average, 22 % at
-// worst; over a quarter of them that a fit to the others left out, 1.4 and 2.0 %.  What
-// the formulas do not see is how uneven the experts are, and that T may be more than
+// worst; over a quarter of them that a fit to the others left out, 1.4 and 2.0 %.  The
+// constants have the shape of what they are named for and no more: none is a measured
+// time or rate by itself.  To fit them again, time every form at such shapes (graphs of
+// 20 calls, weights that do not stay in the caches) and change one constant at a time
+// while the mean of log(time of the chosen form / of the best), plus 0.4 of its root mean
+// square, falls.  What the formulas do not see is how uneven the experts are, and that T may be more than
 // there are rows.
 #include <cmath>
 
@@ -23,13 +27,13 @@ namespace {
 // with per_block falling over `half` of itself to `few`, and the end to nothing, as a
 // round is half full and then empties (where two tiles share a CU, a half is one to
 // each: 1024 x 4096 x 4096 in 256 tiles takes 24 us, in 128 of twice the size 31); no
-// less than the weights of all experts that have rows from memory.
+// less than 2.5 and the weights of all experts that have rows at `memory`.
 // `look`: for the tile of an expert.  `split`: what K % 128 != 0 adds to a block, whose
 // rows then lie across two cache lines.
 struct TileCost {
   Int8Form form;
   int bn, bm, at_once;
-  float start, per_block, few, half, memory, look, end, split;  // memory in TB/s
+  float start, per_block, few, half, memory, look, end, split;  // memory: 10^6 bytes a microsecond, as fitted
 };
 const TileCost kTiles[] = {{kI8Tile256, 256, 256, 256, 7.76f, 1.58f, 0.121f, 0.83f, 3.87f, 0.367f, 0.026f, 0.0115f},
                            {kI8Tile256x128, 256, 128, 256, 3.47f, 0.903f, 0.598f, 0.669f, 5.44f, 0.177f, 1.2f, 0.246f},
