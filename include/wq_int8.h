@@ -48,7 +48,7 @@ wq_status wq_int8_quantize_act(const void* X, int64_t ldx, int64_t M, int64_t K,
  * Gated activation with a quantized result: GU holds rows of 2 K bf16 values
  * (row m at GU + m * ldg elements; ldg >= 2 K, ldg % 8 == 0), gate first;
  *   y[k] = silu(GU[m][k]) * GU[m][K + k],  silu(g) = g / (1 + exp(-g))
- * in fp32, y within 10 * 2^-24 of itself, as far as exp(-g) is a number in fp32;
+ * in fp32, y within 10 * 2^-24 of itself (or of 2^-126), as far as exp(-g) is a number in fp32;
  * beyond (g < -88.72) it is -0, as the fp32 formula has it.  Infinite gates spoil
  * their row: y is an infinity or a NaN.  Xq/Xs receive y quantized.
  */
